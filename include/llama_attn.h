@@ -21,6 +21,9 @@
  * Entry points:
  *   llama_rope_table            cos/sin tables from positions (theta, linear factor)
  *   llama_rope_table_ntk        the same with NTK-aware base scaling
+ *   llama_rope_table_banded     the same with frequencies scaled by wavelength band
+ *   llama_rope_table_yarn       the same with frequencies scaled by a ramp over the dimensions
+ *   llama_rope_apply            rotate q and k by a table (or its transpose: the gradient)
  *   llama_attn_qkv_rope         q/k/v projection GEMM with RoPE in its epilogue
  *   llama_attn_out_proj         output projection GEMM
  *   llama_attn_prefill          full-sequence attention (causal or not, optional mask)
@@ -30,6 +33,7 @@
  *   llama_attn_decode           one query token per sequence against a KV cache
  *   llama_attn_decode_append    the same step with the token's own K/V appended
  *   llama_attn_decode_noalloc   decode on a static scratch (no caller workspace)
+ *   llama_attn_decode_prefix    decode for a batch whose sequences share a prefix
  *   plus workspace sizes, the device status word, failure-detection
  *   self-tests, status strings, ABI version.
  *
@@ -113,6 +117,75 @@ int llama_rope_table(const long long* pos, int bsz, int seq, int head_dim, doubl
  */
 int llama_rope_table_ntk(const long long* pos, int bsz, int seq, int head_dim, double theta,
                          double alpha, float* cos, float* sin, void* cuda_stream);
+
+/*
+ * RoPE tables scaled for contexts longer than the model was trained on.  Both
+ * take the plain frequencies w_i = theta^(-2i/head_dim), i < head_dim/2, and
+ * keep the fast ones, which turn many times within the trained length, while
+ * the slow ones are divided by `factor`; they differ in how the two are told
+ * apart.  Angles are formed in fp64 from pos * w'_i; rows are laid out as
+ * llama_rope_table writes them.  head_dim is the number of rotated dimensions
+ * (a part of the head, if only that is rotated).
+ *
+ * llama_rope_table_banded: by the number of turns over the trained length,
+ *   turns_i = original_len * w_i / (2 pi)
+ *   keep_i  = clamp((turns_i - low_freq_factor) /
+ *                   (high_freq_factor - low_freq_factor), 0, 1)
+ *   w'_i    = w_i * (keep_i + (1 - keep_i) / factor)
+ *
+ * llama_rope_table_yarn (the published YaRN rule): by a ramp over the index i
+ * between the dimensions whose frequencies make beta_fast and beta_slow turns,
+ *   d(beta) = head_dim * ln(original_len / (2 pi beta)) / (2 ln theta)
+ *   lo = max(floor(d(beta_fast)), 0), hi = min(ceil(d(beta_slow)), head_dim - 1)
+ *   ramp_i  = clamp((i - lo) / max(hi - lo, 0.001), 0, 1)
+ *   w'_i    = w_i * (ramp_i / factor + 1 - ramp_i)
+ * and cos and sin are multiplied by attn_factor (the rule's own value is
+ * 0.1 ln(factor) + 1, which sharpens the softmax of longer contexts).
+ *
+ * Errors: as llama_rope_table, plus INVALID_ARG for a factor < 1, an
+ * original_len that is not positive, high_freq_factor <= low_freq_factor or a
+ * negative low_freq_factor (banded); theta <= 1, beta_slow <= 0, beta_fast <=
+ * beta_slow or attn_factor <= 0 (yarn); a value that is not finite;
+ * UNSUPPORTED for head_dim > 512.
+ */
+int llama_rope_table_banded(const long long* pos, int bsz, int seq, int head_dim, double theta,
+                            double factor, double low_freq_factor, double high_freq_factor,
+                            double original_len, float* cos, float* sin, void* cuda_stream);
+int llama_rope_table_yarn(const long long* pos, int bsz, int seq, int head_dim, double theta,
+                          double factor, double beta_fast, double beta_slow, double original_len,
+                          double attn_factor, float* cos, float* sin, void* cuda_stream);
+
+/*
+ * Rotates q and k by a cos/sin table in one launch: every head of every token
+ * by the token's row.  With R = rotary_dim, the first R dimensions of a head
+ * are R/2 pairs, pair i being (x[i], x[i + R/2]), or (x[2i], x[2i + 1]) if
+ * `interleaved`, and
+ *   (a, z) -> (a cos_i - z sin_i, z cos_i + a sin_i),
+ * or with `transpose` (a cos_i + z sin_i, z cos_i - a sin_i): the transposed
+ * map, which takes the gradient of the output to the gradient of the input.
+ * The dimensions from R on are copied.  Arithmetic is fp32, rounded once.
+ *   q            [bsz, seq, n_heads, head_dim]
+ *   k            [bsz, seq, n_kv_heads, head_dim], or NULL (with k_out): q alone
+ *   cos, sin     fp32 [bsz, seq, rotary_dim] table rows (columns i < R/2 are
+ *                read; both pair layouts use the same table)
+ *   q_out, k_out as q and k; may be q and k themselves (with the same strides),
+ *                and may not overlap them otherwise
+ *   *_strides    host arrays of three strides in elements, of batch entry, token
+ *                and head (the dimensions of a head are adjacent), so that q and
+ *                k may be parts of a fused projection's output and k_out the
+ *                rows of a cache; NULL for contiguous
+ * Errors: INVALID_ARG for a NULL required pointer, one of k and k_out alone, a
+ * size < 1, an odd rotary_dim or one outside 2 .. head_dim, a negative stride,
+ * output strides that make elements coincide, a pointer that is not aligned to
+ * its element (cos and sin: to 16 bytes), unknown dtype, more than 2^31 - 1
+ * tokens.  dtype LLAMA_DT_BF16 or LLAMA_DT_F32.
+ */
+int llama_rope_apply(const void* q, const void* k, const float* cos, const float* sin, int bsz,
+                     int seq, int n_heads, int n_kv_heads, int head_dim, int rotary_dim,
+                     int interleaved, int transpose, const long long* q_strides,
+                     const long long* k_strides, void* q_out, void* k_out,
+                     const long long* q_out_strides, const long long* k_out_strides, int dtype,
+                     void* cuda_stream);
 
 /*
  * Q/K/V projection with RoPE in the GEMM epilogue ("[HuggingFace Transformers]
@@ -328,6 +401,49 @@ int llama_attn_decode_noalloc(const void* q, const void* k_cache, const void* v_
                               const int* cache_lens, const float* cos, const float* sin, int bsz,
                               int n_heads, int n_kv_heads, int max_cache_len, int head_dim,
                               float scale, void* out, int dtype, void* cuda_stream);
+
+/*
+ * Single-token decode for a batch whose sequences share a prefix: sequence b
+ * attends to the prefix_len rows of the prefix and to its own cached rows,
+ *   out[b, h] = softmax(scale * q[b, h] . [K_prefix; K_b]) [V_prefix; V_b],
+ * in one softmax over both.  The prefix is held and read once for the whole
+ * batch: its products are taken for all query rows of a K/V head together, and
+ * merged with each sequence's own part by the log-sum-exp identity.
+ *   q          [bsz, n_heads, head_dim], already rotated (llama_attn_qkv_rope or
+ *              llama_rope_apply)
+ *   k_new, v_new  [bsz, n_kv_heads, head_dim] the step's own key (already
+ *              rotated) and value, or both NULL.  If given they are written to
+ *              row p = min(max(cache_lens[b], 0), max_cache_len - 1) of the caches
+ *              first, as llama_attn_decode_append does, and rows 0..p attended
+ *   k_prefix, v_prefix  [n_kv_heads, prefix_len, head_dim], keys rotated; may be
+ *              NULL if prefix_len is 0
+ *   *_prefix_strides  host arrays of two strides in elements, of K/V head and row
+ *              (multiples of 8, so that e.g. the [tokens, n_kv_heads, head_dim] of a
+ *              prefill serves as it is); NULL for contiguous
+ *   k_cache, v_cache  [bsz, n_kv_heads, max_cache_len, head_dim]: the rows of each
+ *              sequence after the prefix
+ *   cache_lens device int32 [bsz]: valid cache rows, clamped to [0, max_cache_len]
+ *              on the device.  A sequence with no row of its own attends to the
+ *              prefix alone, and to nothing (zero output) if that is empty too
+ *   out        [bsz, n_heads * head_dim]
+ *   workspace  caller-owned device scratch of at least
+ *              llama_attn_decode_prefix_workspace_bytes(...) bytes
+ * prefix_len is a host value: the prefix is fixed while its batch decodes.
+ * bf16 only.  Errors: as llama_attn_decode, plus INVALID_ARG for one of k_new
+ * and v_new alone, prefix_len < 0, a prefix stride that is not a multiple of 8
+ * or is less than head_dim, and UNSUPPORTED for fp32.
+ */
+int llama_attn_decode_prefix(const void* q, const void* k_new, const void* v_new,
+                             const void* k_prefix, const void* v_prefix, int prefix_len,
+                             const long long* k_prefix_strides, const long long* v_prefix_strides,
+                             void* k_cache, void* v_cache, const int* cache_lens, int bsz,
+                             int n_heads, int n_kv_heads, int max_cache_len, int head_dim,
+                             float scale, void* out, void* workspace, size_t workspace_bytes,
+                             int dtype, void* cuda_stream);
+
+/* Device bytes of workspace llama_attn_decode_prefix needs. */
+size_t llama_attn_decode_prefix_workspace_bytes(int bsz, int n_heads, int n_kv_heads,
+                                                int prefix_len, int head_dim);
 
 /* Synchronises `cuda_stream`, then reads and clears the device status word of
  * the current device.  Returns LLAMA_OK, LLAMA_ERR_DEVICE_TIMEOUT, or

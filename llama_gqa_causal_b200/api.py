@@ -38,6 +38,9 @@ LLAMA_ERR_DEVICE_TIMEOUT = 4
 EXPORTED = (
     "llama_rope_table",
     "llama_rope_table_ntk",
+    "llama_rope_table_banded",
+    "llama_rope_table_yarn",
+    "llama_rope_apply",
     "llama_attn_qkv_rope",
     "llama_attn_out_proj",
     "llama_attn_prefill_workspace_bytes",
@@ -49,6 +52,8 @@ EXPORTED = (
     "llama_attn_decode",
     "llama_attn_decode_append",
     "llama_attn_decode_noalloc",
+    "llama_attn_decode_prefix_workspace_bytes",
+    "llama_attn_decode_prefix",
     "llama_attn_device_status",
     "llama_attn_selftest_wait_timeout",
     "llama_attn_selftest_launch_error",
@@ -89,6 +94,12 @@ def load() -> ctypes.CDLL:
     lib.llama_rope_table.restype = I
     lib.llama_rope_table_ntk.argtypes = [P, I, I, I, D, D, P, P, P]
     lib.llama_rope_table_ntk.restype = I
+    lib.llama_rope_table_banded.argtypes = [P, I, I, I, D, D, D, D, D, P, P, P]
+    lib.llama_rope_table_banded.restype = I
+    lib.llama_rope_table_yarn.argtypes = [P, I, I, I, D, D, D, D, D, D, P, P, P]
+    lib.llama_rope_table_yarn.restype = I
+    lib.llama_rope_apply.argtypes = [P, P, P, P, I, I, I, I, I, I, I, I, P, P, P, P, P, P, I, P]
+    lib.llama_rope_apply.restype = I
     lib.llama_attn_qkv_rope.argtypes = [P, P, P, P, I, I, I, I, I, P, P, P, I, P]
     lib.llama_attn_qkv_rope.restype = I
     lib.llama_attn_out_proj.argtypes = [P, P, I, I, I, P, I, P]
@@ -111,6 +122,11 @@ def load() -> ctypes.CDLL:
     lib.llama_attn_decode_append.restype = I
     lib.llama_attn_decode_noalloc.argtypes = [P, P, P, P, P, P, I, I, I, I, I, F, P, I, P]
     lib.llama_attn_decode_noalloc.restype = I
+    lib.llama_attn_decode_prefix_workspace_bytes.argtypes = [I, I, I, I, I]
+    lib.llama_attn_decode_prefix_workspace_bytes.restype = Z
+    lib.llama_attn_decode_prefix.argtypes = [P, P, P, P, P, I, P, P, P, P, P, I, I, I, I, I, F, P, P, Z,
+                                             I, P]
+    lib.llama_attn_decode_prefix.restype = I
     lib.llama_attn_device_status.argtypes = [P]
     lib.llama_attn_device_status.restype = I
     lib.llama_attn_selftest_wait_timeout.argtypes = [ctypes.c_uint, P]
@@ -209,6 +225,111 @@ def rope_table_ntk(pos: torch.Tensor, head_dim: int, theta: float = 10000.0, alp
     _check(lib.llama_rope_table_ntk(_ptr(pos), bsz, seq, head_dim, float(theta), float(alpha),
                                     _ptr(cos), _ptr(sin), _stream(stream)), "llama_rope_table_ntk")
     return cos, sin
+
+
+def _on(device: torch.device, where: str, fn, args, stream):
+    """Call a library function on the tensors' own device: a launch goes to the
+    current device, which need not be theirs."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)), where)
+        return
+    with torch.cuda.device(device):
+        _check(fn(*args, _stream(stream)), where)
+
+
+def _table_scaled(where: str, pos: torch.Tensor, head_dim: int, args, stream):
+    fn = getattr(load(), where)
+    pos = pos.to(torch.int64).contiguous()
+    p = _ptr(pos)
+    cos = torch.empty(*pos.shape, head_dim, device=pos.device, dtype=torch.float32)
+    sin = torch.empty_like(cos)
+    n = pos.numel()
+    bsz = pos.shape[0] if pos.dim() > 1 else 1
+    _on(pos.device, where, fn, (p, bsz, n // max(bsz, 1), head_dim, *args, cos.data_ptr(),
+                                sin.data_ptr()), stream)
+    return cos, sin
+
+
+def rope_table_banded(pos: torch.Tensor, head_dim: int, theta: float = 10000.0, *, factor: float,
+                      original_len: float, low_freq_factor: float = 1.0,
+                      high_freq_factor: float = 4.0, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """cos, sin [*pos.shape, head_dim] fp32 of the table scaled by wavelength band
+    (llama_rope_table_banded): frequencies that turn more than high_freq_factor times
+    over original_len are kept, those below low_freq_factor divided by factor."""
+    return _table_scaled("llama_rope_table_banded", pos, head_dim,
+                         (theta, factor, low_freq_factor, high_freq_factor, original_len), stream)
+
+
+def rope_table_yarn(pos: torch.Tensor, head_dim: int, theta: float = 10000.0, *, factor: float,
+                    original_len: float, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                    attn_factor: Optional[float] = None,
+                    stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """cos, sin of the YaRN table (llama_rope_table_yarn); attn_factor, which multiplies
+    both, is 0.1 ln(factor) + 1 unless given."""
+    if attn_factor is None:
+        attn_factor = 0.1 * math.log(factor) + 1.0 if factor > 0.0 else 1.0
+    return _table_scaled("llama_rope_table_yarn", pos, head_dim,
+                         (theta, factor, beta_fast, beta_slow, original_len, attn_factor), stream)
+
+
+_Strides = ctypes.c_longlong * 3
+_PrefixStrides = ctypes.c_longlong * 2
+
+
+def _rope_view(t: torch.Tensor, where: str, name: str, dtype, device, tokens):
+    """(pointer, strides of batch entry, token and head) of [b, s, heads, D] or [s, heads, D]."""
+    if not t.is_cuda:
+        raise ValueError("llama_attn: tensors must live on a CUDA device")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{where}: {name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    if t.shape[:-2] != tokens or t.dim() != len(tokens) + 2:
+        raise ValueError(f"{where}: {name} must be [{', '.join(map(str, tokens))}, heads, head_dim], "
+                         f"got {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{where}: the dimensions of a head of {name} must be adjacent")
+    return t.data_ptr(), _Strides(st[0] if len(st) == 4 else 0, st[-3], st[-2])
+
+
+def rope_apply(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, sin: torch.Tensor, *,
+               interleaved: bool = False, transpose: bool = False, out=None,
+               stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """llama_rope_apply.  q [b, s, H, D] or [s, H, D], k likewise with its own heads (or
+    None), rotated by the rows of cos, sin [.., R], R <= D.  Both may be strided views
+    (parts of a fused projection), and so may out, a pair of tensors (q and k themselves:
+    in place; k's: rows of a cache).  transpose: the gradient of the rotation."""
+    w = "llama_rope_apply"
+    fn = load().llama_rope_apply
+    if q.dim() not in (3, 4):
+        raise ValueError(f"{w}: q must be [b, s, heads, head_dim] or [s, heads, head_dim]")
+    tokens, H, D = q.shape[:-2], q.shape[-2], q.shape[-1]
+    b, s = tokens if len(tokens) == 2 else (1, tokens[0])
+    R = cos.shape[-1]
+    dev, dt = q.device, q.dtype
+    _tables(cos, sin, w, dev, b * s, R)
+    if sin.shape != cos.shape:
+        raise ValueError(f"{w}: cos and sin must have one shape")
+    qp, qs = _rope_view(q, w, "q", dt, dev, tokens)
+    q_out, k_out = out if out is not None else (None, None)
+    if q_out is None:
+        q_out = torch.empty(q.shape, device=dev, dtype=dt)
+    elif q_out.shape != q.shape:
+        raise ValueError(f"{w}: out must have the shapes of q and k")
+    qop, qos = _rope_view(q_out, w, "out", dt, dev, tokens)
+    Hkv = kp = ks = kop = kos = None
+    if k is not None:
+        kp, ks = _rope_view(k, w, "k", dt, dev, tokens)
+        Hkv = k.shape[-2]
+        if k_out is None:
+            k_out = torch.empty(k.shape, device=dev, dtype=dt)
+        if k.shape[-1] != D or k_out.shape != k.shape:
+            raise ValueError(f"{w}: k must have q's head_dim, and out the shapes of q and k")
+        kop, kos = _rope_view(k_out, w, "out", dt, dev, tokens)
+    elif k_out is not None:
+        raise ValueError(f"{w}: an output for k needs k")
+    _on(dev, w, fn, (qp, kp, _ptr(cos), _ptr(sin), b, s, H, Hkv or 0, D, R, int(bool(interleaved)),
+                     int(bool(transpose)), qs, ks, qop, kop, qos, kos, _dtype_code(dt)), stream)
+    return q_out, k_out
 
 
 def qkv_rope(x: torch.Tensor, w_qkv: torch.Tensor, n_heads: int, n_kv_heads: int, head_dim: int,
@@ -477,6 +598,62 @@ def decode_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                                          _ptr(cos), _ptr(sin), b, H, Hkv, L, D, float(scale),
                                          _ptr(out), _dtype_code(q.dtype), _stream(stream)),
            "llama_attn_decode_noalloc")
+    return out
+
+
+def decode_prefix_workspace_bytes(bsz, n_heads, n_kv_heads, prefix_len, head_dim) -> int:
+    return int(load().llama_attn_decode_prefix_workspace_bytes(bsz, n_heads, n_kv_heads, prefix_len,
+                                                               head_dim))
+
+
+def _prefix_view(t: torch.Tensor, name: str, like: torch.Tensor, Hkv: int, P: int, D: int):
+    """(pointer, strides of K/V head and row) of a prefix tensor [Hkv, P, D]."""
+    w = "llama_attn_decode_prefix"
+    if not t.is_cuda:
+        raise ValueError("llama_attn: tensors must live on a CUDA device")
+    _need(t, w, name, like.dtype, like.device, shape=(Hkv, P, D))
+    st = t.stride()
+    if st[2] != 1:
+        raise ValueError(f"{w}: the dimensions of a row of {name} must be adjacent")
+    # the stride of an extent of one is never used; torch leaves it arbitrary
+    row = st[1] if P > 1 else D
+    return t.data_ptr(), _PrefixStrides(st[0] if Hkv > 1 else P * row, row)
+
+
+def decode_prefix(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor,
+                  k_cache: torch.Tensor, v_cache: torch.Tensor, cache_lens: torch.Tensor, *,
+                  k_new: Optional[torch.Tensor] = None, v_new: Optional[torch.Tensor] = None,
+                  scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """llama_attn_decode_prefix.  q [b,H,D] (rotated), the shared prefix [Hkv,P,D] (keys
+    rotated; a strided view is taken as it is), caches [b,Hkv,L,D] of the rows after it,
+    cache_lens int32 [b] -> out [b, H*D].  With k_new, v_new [b,Hkv,D] (k_new rotated)
+    the step's own row is appended to the caches first."""
+    w = "llama_attn_decode_prefix"
+    fn = load().llama_attn_decode_prefix
+    b, H, D = q.shape
+    Hkv, L = k_cache.shape[1], k_cache.shape[2]
+    P = k_prefix.shape[1]
+    dev = q.device
+    _need(k_cache, w, "k_cache", q.dtype, dev, shape=(b, Hkv, L, D))
+    _need(v_cache, w, "v_cache", q.dtype, dev, shape=(b, Hkv, L, D))
+    _need(cache_lens, w, "cache_lens", torch.int32, dev, numel=b)
+    _need(k_new, w, "k_new", q.dtype, dev, shape=(b, Hkv, D))
+    _need(v_new, w, "v_new", q.dtype, dev, shape=(b, Hkv, D))
+    _need(out, w, "out", q.dtype, dev, numel=b * H * D)
+    kp, ks = _prefix_view(k_prefix, "k_prefix", q, Hkv, P, D)
+    vp, vs = _prefix_view(v_prefix, "v_prefix", q, Hkv, P, D)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty(b, H * D, device=dev, dtype=q.dtype)
+    if workspace is None:
+        workspace = torch.empty(decode_prefix_workspace_bytes(b, H, Hkv, P, D), device=dev,
+                                dtype=torch.uint8)
+    ws_bytes = workspace.numel() * workspace.element_size()
+    _on(dev, w, fn, (_ptr(q), _ptr(k_new), _ptr(v_new), kp, vp, P, ks, vs, _ptr(k_cache),
+                     _ptr(v_cache), _ptr(cache_lens), b, H, Hkv, L, D, scale, _ptr(out),
+                     _ptr(workspace), ws_bytes, _dtype_code(q.dtype)), stream)
     return out
 
 

@@ -8,15 +8,18 @@
 #include <algorithm>
 #include <cmath>
 #include <mutex>
+#include <utility>
 
 #include "llama_attn.h"
 
 #include "common.cuh"
 #include "attn_fp32.cuh"
 #include "decode_bf16.cuh"
+#include "decode_prefix.cuh"
 #include "gemm_sm100.cuh"
 #include "prefill_sm100.cuh"
 #include "rope.cuh"
+#include "rope_apply.cuh"
 
 namespace {
 
@@ -395,6 +398,72 @@ int decode_bf16(const void* q, const void* kc, const void* vc, const int* lens, 
   return launch_status();
 }
 
+// ---------------------------------------------------------------- scaled tables and rotation
+// The table of rows cos, sin (pos * inv[i]) * gain for frequencies made here.
+int rope_table_scaled(const long long* pos, int bsz, int seq, int head_dim, double gain, float* cos,
+                      float* sin, const la::ScaledFreqs& freqs, cudaStream_t st) {
+  const long long n = static_cast<long long>(bsz) * seq;
+  const int half = head_dim / 2;
+  const long long work = n * half;
+  const int blocks = static_cast<int>(
+      std::min<long long>((work + la::ra::THREADS - 1) / la::ra::THREADS, 148LL * 32));
+  la::rope_table_scaled_kernel<<<blocks, la::ra::THREADS, 0, st>>>(pos, n, half, gain, cos, sin,
+                                                                   freqs);
+  return launch_status();
+}
+
+int check_table_scaled(const long long* pos, int bsz, int seq, int head_dim, double theta,
+                       double factor, double original_len, const float* cos, const float* sin) {
+  if (!pos || !cos || !sin) return LLAMA_ERR_INVALID_ARG;
+  if (bsz < 1 || seq < 1 || head_dim < 2 || (head_dim % 2)) return LLAMA_ERR_INVALID_ARG;
+  if (!(theta > 0.0) || !std::isfinite(theta) || !(factor >= 1.0) || !std::isfinite(factor) ||
+      !(original_len > 0.0) || !std::isfinite(original_len))
+    return LLAMA_ERR_INVALID_ARG;
+  if (head_dim > 2 * la::ra::kMaxHalf) return LLAMA_ERR_UNSUPPORTED;
+  return LLAMA_OK;
+}
+
+constexpr double kPi = 3.14159265358979323846;
+
+// Fills in one tensor of a rotation; false for strides that are negative or
+// that make two output elements one (checked with the extents in the order of
+// their strides, each of which has to step over all that lies below it).
+bool rope_side(la::RopeSide* sd, const void* x, const long long* xs, void* y, const long long* ys,
+               int bsz, int seq, int heads, int D) {
+  sd->x = x;
+  sd->y = y;
+  sd->heads = heads;
+  const long long dense[3] = {static_cast<long long>(seq) * heads * D,
+                              static_cast<long long>(heads) * D, D};
+  if (!xs) xs = dense;
+  if (!ys) ys = dense;
+  for (int i = 0; i < 3; ++i)
+    if (xs[i] < 0 || ys[i] < 0) return false;
+  if (heads > 0) {
+    std::pair<long long, long long> dim[3] = {{ys[0], bsz}, {ys[1], seq}, {ys[2], heads}};
+    std::sort(dim, dim + 3);
+    long long span = D;
+    for (const auto& d : dim) {
+      if (d.second == 1) continue;
+      if (d.first < span || d.first > (1LL << 48)) return false;
+      span += (d.second - 1) * d.first;
+    }
+  }
+  sd->xb = xs[0], sd->xs = xs[1], sd->xh = xs[2];
+  sd->yb = ys[0], sd->ys = ys[1], sd->yh = ys[2];
+  return true;
+}
+
+template <typename T>
+int rope_apply(const la::RopeApplyParams& p, int interleaved, cudaStream_t st) {
+  const long long work = p.tokens * (p.side[0].heads + p.side[1].heads) * (p.D - p.R / 2);
+  const int blocks = static_cast<int>(
+      std::min<long long>((work + la::ra::THREADS - 1) / la::ra::THREADS, 148LL * 32));
+  if (interleaved) la::rope_apply_any_kernel<T, true><<<blocks, la::ra::THREADS, 0, st>>>(p);
+  else la::rope_apply_any_kernel<T, false><<<blocks, la::ra::THREADS, 0, st>>>(p);
+  return launch_status();
+}
+
 // ---------------------------------------------------------------- failure-detection self-tests
 // A warp waits on an mbarrier that nothing ever arrives on, with a short
 // limit: the wait runs out, records the timeout in the device status word
@@ -498,6 +567,82 @@ int llama_rope_table_ntk(const long long* pos, int bsz, int seq, int head_dim, d
   const double base = theta * std::pow(alpha, static_cast<double>(head_dim) / (head_dim - 2));
   if (!std::isfinite(base)) return LLAMA_ERR_INVALID_ARG;
   return llama_rope_table(pos, bsz, seq, head_dim, base, 1.0, cos, sin, cuda_stream);
+}
+
+int llama_rope_table_banded(const long long* pos, int bsz, int seq, int head_dim, double theta,
+                            double factor, double low_freq_factor, double high_freq_factor,
+                            double original_len, float* cos, float* sin, void* cuda_stream) {
+  if (int e = check_table_scaled(pos, bsz, seq, head_dim, theta, factor, original_len, cos, sin))
+    return e;
+  if (!(low_freq_factor >= 0.0) || !(high_freq_factor > low_freq_factor) ||
+      !std::isfinite(high_freq_factor))
+    return LLAMA_ERR_INVALID_ARG;
+  la::ScaledFreqs freqs;
+  for (int i = 0; i < head_dim / 2; ++i) {
+    const double w = std::exp(-(2.0 * i / head_dim) * std::log(theta));
+    const double turns = original_len * w / (2.0 * kPi);
+    const double keep = std::min(
+        1.0, std::max(0.0, (turns - low_freq_factor) / (high_freq_factor - low_freq_factor)));
+    freqs.inv[i] = w * (keep + (1.0 - keep) / factor);
+  }
+  return rope_table_scaled(pos, bsz, seq, head_dim, 1.0, cos, sin, freqs, as_stream(cuda_stream));
+}
+
+int llama_rope_table_yarn(const long long* pos, int bsz, int seq, int head_dim, double theta,
+                          double factor, double beta_fast, double beta_slow, double original_len,
+                          double attn_factor, float* cos, float* sin, void* cuda_stream) {
+  if (int e = check_table_scaled(pos, bsz, seq, head_dim, theta, factor, original_len, cos, sin))
+    return e;
+  if (!(theta > 1.0) || !(beta_slow > 0.0) || !(beta_fast > beta_slow) ||
+      !std::isfinite(beta_fast) || !(attn_factor > 0.0) || !std::isfinite(attn_factor))
+    return LLAMA_ERR_INVALID_ARG;
+  auto dim_of = [&](double beta) {
+    return head_dim * std::log(original_len / (2.0 * kPi * beta)) / (2.0 * std::log(theta));
+  };
+  const double lo = std::max(std::floor(dim_of(beta_fast)), 0.0);
+  const double hi = std::min(std::ceil(dim_of(beta_slow)), static_cast<double>(head_dim - 1));
+  la::ScaledFreqs freqs;
+  for (int i = 0; i < head_dim / 2; ++i) {
+    const double w = std::exp(-(2.0 * i / head_dim) * std::log(theta));
+    const double ramp = std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 0.001)));
+    freqs.inv[i] = w * (ramp / factor + (1.0 - ramp));
+  }
+  return rope_table_scaled(pos, bsz, seq, head_dim, attn_factor, cos, sin, freqs,
+                           as_stream(cuda_stream));
+}
+
+int llama_rope_apply(const void* q, const void* k, const float* cos, const float* sin, int bsz,
+                     int seq, int n_heads, int n_kv_heads, int head_dim, int rotary_dim,
+                     int interleaved, int transpose, const long long* q_strides,
+                     const long long* k_strides, void* q_out, void* k_out,
+                     const long long* q_out_strides, const long long* k_out_strides, int dtype,
+                     void* cuda_stream) {
+  if (!q || !q_out || !cos || !sin || (k == nullptr) != (k_out == nullptr))
+    return LLAMA_ERR_INVALID_ARG;
+  if (bsz < 1 || seq < 1 || n_heads < 1 || (k && n_kv_heads < 1) || head_dim < 2)
+    return LLAMA_ERR_INVALID_ARG;
+  if (rotary_dim < 2 || (rotary_dim % 2) || rotary_dim > head_dim) return LLAMA_ERR_INVALID_ARG;
+  if (dtype != LLAMA_DT_F32 && dtype != LLAMA_DT_BF16) return LLAMA_ERR_INVALID_ARG;
+  const uintptr_t low = dtype == LLAMA_DT_F32 ? 3u : 1u;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) |
+       reinterpret_cast<uintptr_t>(q_out) | reinterpret_cast<uintptr_t>(k_out)) & low)
+    return LLAMA_ERR_INVALID_ARG;
+  if (!aligned16(cos) || !aligned16(sin)) return LLAMA_ERR_INVALID_ARG;
+  la::RopeApplyParams p;
+  p.tokens = static_cast<long long>(bsz) * seq;
+  if (p.tokens > 0x7fffffffLL) return LLAMA_ERR_INVALID_ARG;
+  if (!rope_side(&p.side[0], q, q_strides, q_out, q_out_strides, bsz, seq, n_heads, head_dim) ||
+      !rope_side(&p.side[1], k, k_strides, k_out, k_out_strides, bsz, seq, k ? n_kv_heads : 0,
+                 head_dim))
+    return LLAMA_ERR_INVALID_ARG;
+  p.cos = cos;
+  p.sin = sin;
+  p.seq = seq;
+  p.D = head_dim;
+  p.R = rotary_dim;
+  p.sign = transpose ? -1.f : 1.f;
+  if (dtype == LLAMA_DT_F32) return rope_apply<float>(p, interleaved, as_stream(cuda_stream));
+  return rope_apply<__nv_bfloat16>(p, interleaved, as_stream(cuda_stream));
 }
 
 int llama_attn_qkv_rope(const void* x, const void* w_qkv, const float* cos, const float* sin,
@@ -745,6 +890,66 @@ int llama_attn_decode_noalloc(const void* q, const void* k_cache, const void* v_
   return llama_attn_decode(q, k_cache, v_cache, cache_lens, cos, sin, bsz, n_heads, n_kv_heads,
                            max_cache_len, head_dim, scale, out, scratch,
                            scratch ? kNoAllocScratchBytes : 0, dtype, cuda_stream);
+}
+
+size_t llama_attn_decode_prefix_workspace_bytes(int bsz, int n_heads, int n_kv_heads,
+                                                int prefix_len, int head_dim) {
+  if (bsz < 1 || n_heads < 1 || n_kv_heads < 1 || prefix_len < 0 || head_dim < 1) return 0;
+  return 256;
+}
+
+int llama_attn_decode_prefix(const void* q, const void* k_new, const void* v_new,
+                             const void* k_prefix, const void* v_prefix, int prefix_len,
+                             const long long* k_prefix_strides, const long long* v_prefix_strides,
+                             void* k_cache, void* v_cache, const int* cache_lens, int bsz,
+                             int n_heads, int n_kv_heads, int max_cache_len, int head_dim,
+                             float scale, void* out, void* workspace, size_t workspace_bytes,
+                             int dtype, void* cuda_stream) {
+  if (!q || !k_cache || !v_cache || !cache_lens || !out || prefix_len < 0)
+    return LLAMA_ERR_INVALID_ARG;
+  if ((k_new == nullptr) != (v_new == nullptr)) return LLAMA_ERR_INVALID_ARG;
+  if (prefix_len > 0 && (!k_prefix || !v_prefix)) return LLAMA_ERR_INVALID_ARG;
+  if (max_cache_len < 1) return LLAMA_ERR_INVALID_ARG;
+  if (int e = check_common(bsz, n_heads, n_kv_heads, head_dim, dtype, nullptr, nullptr, scale))
+    return e;
+  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_prefix) ||
+      !aligned16(v_prefix) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+      !aligned16(workspace) || (reinterpret_cast<uintptr_t>(cache_lens) & 3u))
+    return LLAMA_ERR_INVALID_ARG;
+  const long long dense[2] = {static_cast<long long>(prefix_len) * head_dim, head_dim};
+  const long long* ks = k_prefix_strides ? k_prefix_strides : dense;
+  const long long* vs = v_prefix_strides ? v_prefix_strides : dense;
+  if (prefix_len > 0)
+    for (int i = 0; i < 2; ++i)
+      if (ks[i] % 8 || vs[i] % 8 || ks[i] < head_dim || vs[i] < head_dim)
+        return LLAMA_ERR_INVALID_ARG;
+  if (dtype != LLAMA_DT_BF16) return LLAMA_ERR_UNSUPPORTED;
+  if (bsz > la::dec::MAX_BATCH) return LLAMA_ERR_UNSUPPORTED;
+  const size_t need = llama_attn_decode_prefix_workspace_bytes(bsz, n_heads, n_kv_heads, prefix_len,
+                                                               head_dim);
+  if (workspace == nullptr || workspace_bytes < need) return LLAMA_ERR_INVALID_ARG;
+  la::DecodePrefixParams p;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_pre = static_cast<const __nv_bfloat16*>(k_prefix);
+  p.v_pre = static_cast<const __nv_bfloat16*>(v_prefix);
+  p.kp_head = ks[0], p.kp_row = ks[1], p.vp_head = vs[0], p.vp_row = vs[1];
+  p.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  p.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  p.k_cache = static_cast<__nv_bfloat16*>(k_cache);
+  p.v_cache = static_cast<__nv_bfloat16*>(v_cache);
+  p.lens = cache_lens;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.prefix_len = prefix_len;
+  p.H = n_heads;
+  p.Hkv = n_kv_heads;
+  p.L = max_cache_len;
+  p.group = n_heads / n_kv_heads;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  const dim3 grid(n_heads, bsz);
+  cudaStream_t st = as_stream(cuda_stream);
+  if (head_dim == 128) la::decode_prefix_plain_kernel<128><<<grid, 128, 0, st>>>(p);
+  else la::decode_prefix_plain_kernel<64><<<grid, 128, 0, st>>>(p);
+  return launch_status();
 }
 
 int llama_attn_selftest_wait_timeout(unsigned int limit_us, void* cuda_stream) {
