@@ -399,17 +399,45 @@ int decode_bf16(const void* q, const void* kc, const void* vc, const int* lens, 
 }
 
 // ---------------------------------------------------------------- scaled tables and rotation
-// The table of rows cos, sin (pos * inv[i]) * gain for frequencies made here.
+// Launches as a programmatic dependent of what precedes it on the stream (the
+// kernel waits on the device before it touches memory).
+template <typename... P, typename... A>
+int launch_dependent(void (*kernel)(P...), long long blocks, int threads, cudaStream_t st,
+                     const char* what, const A&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+  if (e != cudaSuccess) {
+    fprintf(stderr, "llama_attn: %s launch failed: %s\n", what, cudaGetErrorString(e));
+    (void)cudaGetLastError();  // reported here, not again by a later call
+    return LLAMA_ERR_CUDA;
+  }
+  return launch_status();
+}
+
+// The table of rows cos, sin (pos * inv[i]) * gain for frequencies made by the caller.
 int rope_table_scaled(const long long* pos, int bsz, int seq, int head_dim, double gain, float* cos,
                       float* sin, const la::ScaledFreqs& freqs, cudaStream_t st) {
   const long long n = static_cast<long long>(bsz) * seq;
   const int half = head_dim / 2;
-  const long long work = n * half;
-  const int blocks = static_cast<int>(
-      std::min<long long>((work + la::ra::THREADS - 1) / la::ra::THREADS, 148LL * 32));
-  la::rope_table_scaled_kernel<<<blocks, la::ra::THREADS, 0, st>>>(pos, n, half, gain, cos, sin,
-                                                                   freqs);
-  return launch_status();
+  const bool vec = half % 4 == 0 && aligned16(cos) && aligned16(sin);
+  const int per_row = vec ? half / 4 : half;  // at most 256
+  const int rows = la::ra::THREADS / per_row;
+  // enough blocks to fill the GPU eight times over at most: a thread then
+  // walks its rows with the frequencies it has loaded
+  const long long blocks = std::min<long long>((n + rows - 1) / rows, 148LL * 8);
+  if (vec)
+    return launch_dependent(la::rope_table_scaled_kernel<4>, blocks, rows * per_row, st,
+                            "scaled rope table", pos, n, half, gain, cos, sin, freqs);
+  return launch_dependent(la::rope_table_scaled_kernel<1>, blocks, rows * per_row, st,
+                          "scaled rope table", pos, n, half, gain, cos, sin, freqs);
 }
 
 int check_table_scaled(const long long* pos, int bsz, int seq, int head_dim, double theta,
@@ -425,8 +453,8 @@ int check_table_scaled(const long long* pos, int bsz, int seq, int head_dim, dou
 
 constexpr double kPi = 3.14159265358979323846;
 
-// Fills in one tensor of a rotation; false for strides that are negative or
-// that make two output elements one (checked with the extents in the order of
+// Fills in one tensor of a rotation; false for strides that are negative, that
+// differ between a tensor and itself as the output, or that make two output elements one (checked with the extents in the order of
 // their strides, each of which has to step over all that lies below it).
 bool rope_side(la::RopeSide* sd, const void* x, const long long* xs, void* y, const long long* ys,
                int bsz, int seq, int heads, int D) {
@@ -438,7 +466,7 @@ bool rope_side(la::RopeSide* sd, const void* x, const long long* xs, void* y, co
   if (!xs) xs = dense;
   if (!ys) ys = dense;
   for (int i = 0; i < 3; ++i)
-    if (xs[i] < 0 || ys[i] < 0) return false;
+    if (xs[i] < 0 || ys[i] < 0 || (x == y && xs[i] != ys[i])) return false;
   if (heads > 0) {
     std::pair<long long, long long> dim[3] = {{ys[0], bsz}, {ys[1], seq}, {ys[2], heads}};
     std::sort(dim, dim + 3);
@@ -455,13 +483,32 @@ bool rope_side(la::RopeSide* sd, const void* x, const long long* xs, void* y, co
 }
 
 template <typename T>
-int rope_apply(const la::RopeApplyParams& p, int interleaved, cudaStream_t st) {
+int rope_apply(la::RopeApplyParams& p, int interleaved, cudaStream_t st) {
+  constexpr int VE = 16 / sizeof(T);
+  // the vector kernel works on whole 16-byte chunks: of the head, of its
+  // rotated part (of each half of that, in the half layout) and at every stride
+  bool vec = p.D % VE == 0 && (interleaved ? p.R : p.R / 2) % VE == 0;
+  for (const la::RopeSide& s : p.side)
+    if (s.heads > 0)
+      vec = vec && aligned16(s.x) && aligned16(s.y) &&
+            ((s.xb | s.xs | s.xh | s.yb | s.ys | s.yh) % VE) == 0;
+  if (vec) {
+    for (int i = 0; i < 2; ++i)
+      p.blocks[i] = (p.side[i].heads + la::ra::HB - 1) / la::ra::HB;
+    const int units = (interleaved ? p.R : p.R / 2) / VE + (p.D - p.R) / VE;
+    const long long work = p.tokens * (p.blocks[0] + p.blocks[1]) * units;
+    const long long blocks = (work + la::ra::THREADS - 1) / la::ra::THREADS;
+    if (blocks > 0x7fffffffLL) return LLAMA_ERR_INVALID_ARG;
+    return launch_dependent(interleaved ? la::rope_apply_vec_kernel<T, true>
+                                        : la::rope_apply_vec_kernel<T, false>,
+                            blocks, la::ra::THREADS, st, "rotation", p);
+  }
   const long long work = p.tokens * (p.side[0].heads + p.side[1].heads) * (p.D - p.R / 2);
-  const int blocks = static_cast<int>(
-      std::min<long long>((work + la::ra::THREADS - 1) / la::ra::THREADS, 148LL * 32));
-  if (interleaved) la::rope_apply_any_kernel<T, true><<<blocks, la::ra::THREADS, 0, st>>>(p);
-  else la::rope_apply_any_kernel<T, false><<<blocks, la::ra::THREADS, 0, st>>>(p);
-  return launch_status();
+  const long long blocks =
+      std::min<long long>((work + la::ra::THREADS - 1) / la::ra::THREADS, 148LL * 32);
+  return launch_dependent(interleaved ? la::rope_apply_any_kernel<T, true>
+                                      : la::rope_apply_any_kernel<T, false>,
+                          blocks, la::ra::THREADS, st, "rotation", p);
 }
 
 // ---------------------------------------------------------------- failure-detection self-tests

@@ -73,6 +73,7 @@ APPLY = dict(q=FAKE, k=FAKE, cos=FAKE, sin=FAKE, bsz=2, seq=3, H=4, Hkv=2, D=64,
     dict(qos=strides(768, 256, 63)),    # heads that overlap
     dict(qos=strides(768, 255, 64)),    # tokens that overlap
     dict(kos=strides(1, 128, 64)),
+    dict(qs=strides(768, 256, 128)),    # in place, but with other strides
 ], ids=str)
 def test_rotation_refuses(lib, kw):
     assert _call(lib.llama_rope_apply, APPLY, kw) == INVALID
