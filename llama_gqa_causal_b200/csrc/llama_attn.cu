@@ -398,18 +398,18 @@ int decode_bf16(const void* q, const void* kc, const void* vc, const int* lens, 
   return launch_status();
 }
 
-// ---------------------------------------------------------------- scaled tables and rotation
 // Launches as a programmatic dependent of what precedes it on the stream (the
 // kernel waits on the device before it touches memory).
 template <typename... P, typename... A>
-int launch_dependent(void (*kernel)(P...), long long blocks, int threads, cudaStream_t st,
-                     const char* what, const A&... args) {
+int launch_dependent(void (*kernel)(P...), long long blocks, int threads, size_t smem,
+                     cudaStream_t st, const char* what, const A&... args) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -422,6 +422,107 @@ int launch_dependent(void (*kernel)(P...), long long blocks, int threads, cudaSt
   return launch_status();
 }
 
+// ---------------------------------------------------------------- decode behind a shared prefix
+// Layout of the workspace.
+struct PrefixLayout {
+  int nt, pairs;
+  size_t home, ctas, hdr, bytes;  // offsets of the own rows' partials, the ints, and the end
+};
+PrefixLayout prefix_layout(int bsz, int H, int Hkv, int P, int D) {
+  using namespace la::px;
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  PrefixLayout w;
+  const long long rows = static_cast<long long>(bsz) * (H / Hkv);
+  w.nt = P > 0 ? (P - 1) / BN + 1 : 0;
+  w.pairs = static_cast<int>((rows + 2 * BM - 1) / (2 * BM));
+  const size_t seqs = static_cast<size_t>(w.pairs) * Hkv;
+  const size_t slots = w.nt == 0 ? 0 : seqs + std::min<size_t>(seqs * w.nt, MAX_CTAS);
+  w.home = up(slots * 2 * unit_floats(D) * sizeof(float));
+  const size_t row = la::dec::part_stride(D) * sizeof(float);
+  w.ctas = w.home + up(static_cast<size_t>(bsz) * H * row);
+  w.hdr = w.ctas + up(static_cast<size_t>(MAX_CTAS) * 8 * row);
+  w.bytes = w.hdr + up((HDR + static_cast<size_t>(bsz) + 1) * sizeof(int));
+  return w;
+}
+
+constexpr long long kMaxPrefixStride = 1LL << 39;  // of a tensor map: 2^40 bytes
+
+static_assert(la::prefix_smem_bytes<128>() + 64 <= 227 * 1024 &&
+                  la::prefix_smem_bytes<64>() + 64 <= 227 * 1024,
+              "prefix decode shared memory exceeds 227 KB");
+
+template <int D>
+int decode_prefix(const void* q, const void* k_new, const void* v_new, const void* k_prefix,
+                  const void* v_prefix, int P, const long long* ks, const long long* vs,
+                  void* k_cache, void* v_cache, const int* lens, int bsz, int H, int Hkv, int L,
+                  float scale, void* out, void* workspace, cudaStream_t st) {
+  const PrefixLayout w = prefix_layout(bsz, H, Hkv, P, D);
+  CUtensorMap tkp{}, tvp{}, tk, tv;
+  if (P > 0) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(P),
+                                static_cast<cuuint64_t>(Hkv)};
+    const cuuint64_t kst[2] = {static_cast<cuuint64_t>(ks[1]) * 2, static_cast<cuuint64_t>(ks[0]) * 2};
+    const cuuint64_t vst[2] = {static_cast<cuuint64_t>(vs[1]) * 2, static_cast<cuuint64_t>(vs[0]) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(la::px::BN), 1};
+    if (!make_map(&tkp, k_prefix, 3, dims, kst, box)) return LLAMA_ERR_CUDA;
+    if (!make_map(&tvp, v_prefix, 3, dims, vst, box)) return LLAMA_ERR_CUDA;
+  }
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(L),
+                              static_cast<cuuint64_t>(bsz) * Hkv};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(L) * D * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(la::dec::TR), 1};
+  if (!make_map(&tk, k_cache, 3, dims, strides, box)) return LLAMA_ERR_CUDA;
+  if (!make_map(&tv, v_cache, 3, dims, strides, box)) return LLAMA_ERR_CUDA;
+  const int n_ctas = std::min(sm_count(), la::px::MAX_CTAS);
+  if (n_ctas <= 1) return LLAMA_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  la::PrefixParams x;
+  x.q = static_cast<const __nv_bfloat16*>(q);
+  x.part = reinterpret_cast<float*>(ws);
+  x.hdr = reinterpret_cast<int*>(ws + w.hdr);
+  x.rows = bsz * (H / Hkv);
+  x.P = P;
+  x.nt = w.nt;
+  x.pairs = w.pairs;
+  x.H = H;
+  x.Hkv = Hkv;
+  x.group = H / Hkv;
+  x.scale_log2 = scale * 1.4426950408889634f;
+  la::DecodeParams p{};
+  p.q = x.q;
+  p.lens = lens;
+  p.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  p.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  p.k_cache = static_cast<__nv_bfloat16*>(k_cache);
+  p.v_cache = static_cast<__nv_bfloat16*>(v_cache);
+  p.ws_home = reinterpret_cast<float*>(ws + w.home);
+  p.ws_cta = reinterpret_cast<float*>(ws + w.ctas);
+  p.ws_prefix = x.hdr + la::px::HDR;
+  p.bsz = bsz;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.L = L;
+  p.group = x.group;
+  p.hchunks = (p.group + 7) / 8;
+  p.scale_log2 = x.scale_log2;
+  constexpr size_t smem = la::prefix_smem_bytes<D>();
+  int e;
+  if (k_new != nullptr) {
+    if (!ensure_smem_attr<la::decode_prefix_kernel<D, true>>(smem)) return LLAMA_ERR_CUDA;
+    e = launch_dependent(la::decode_prefix_kernel<D, true>, n_ctas, la::px::THREADS, smem, st,
+                         "prefix decode", tkp, tvp, tk, tv, x, p);
+  } else {
+    if (!ensure_smem_attr<la::decode_prefix_kernel<D, false>>(smem)) return LLAMA_ERR_CUDA;
+    e = launch_dependent(la::decode_prefix_kernel<D, false>, n_ctas, la::px::THREADS, smem, st,
+                         "prefix decode", tkp, tvp, tk, tv, x, p);
+  }
+  if (e) return e;
+  const long long blocks = (static_cast<long long>(x.rows) + 31) / 32 * Hkv * (D / 8);
+  return launch_dependent(la::decode_prefix_combine_kernel<D>, blocks, la::px::COMBINE_WARPS * 32, 0,
+                          st, "prefix combine", x, p, static_cast<__nv_bfloat16*>(out));
+}
+
+// ---------------------------------------------------------------- scaled tables and rotation
 // The table of rows cos, sin (pos * inv[i]) * gain for frequencies made by the caller.
 int rope_table_scaled(const long long* pos, int bsz, int seq, int head_dim, double gain, float* cos,
                       float* sin, const la::ScaledFreqs& freqs, cudaStream_t st) {
@@ -434,9 +535,9 @@ int rope_table_scaled(const long long* pos, int bsz, int seq, int head_dim, doub
   // walks its rows with the frequencies it has loaded
   const long long blocks = std::min<long long>((n + rows - 1) / rows, 148LL * 8);
   if (vec)
-    return launch_dependent(la::rope_table_scaled_kernel<4>, blocks, rows * per_row, st,
+    return launch_dependent(la::rope_table_scaled_kernel<4>, blocks, rows * per_row, 0, st,
                             "scaled rope table", pos, n, half, gain, cos, sin, freqs);
-  return launch_dependent(la::rope_table_scaled_kernel<1>, blocks, rows * per_row, st,
+  return launch_dependent(la::rope_table_scaled_kernel<1>, blocks, rows * per_row, 0, st,
                           "scaled rope table", pos, n, half, gain, cos, sin, freqs);
 }
 
@@ -501,14 +602,14 @@ int rope_apply(la::RopeApplyParams& p, int interleaved, cudaStream_t st) {
     if (blocks > 0x7fffffffLL) return LLAMA_ERR_INVALID_ARG;
     return launch_dependent(interleaved ? la::rope_apply_vec_kernel<T, true>
                                         : la::rope_apply_vec_kernel<T, false>,
-                            blocks, la::ra::THREADS, st, "rotation", p);
+                            blocks, la::ra::THREADS, 0, st, "rotation", p);
   }
   const long long work = p.tokens * (p.side[0].heads + p.side[1].heads) * (p.D - p.R / 2);
   const long long blocks =
       std::min<long long>((work + la::ra::THREADS - 1) / la::ra::THREADS, 148LL * 32);
   return launch_dependent(interleaved ? la::rope_apply_any_kernel<T, true>
                                       : la::rope_apply_any_kernel<T, false>,
-                          blocks, la::ra::THREADS, st, "rotation", p);
+                          blocks, la::ra::THREADS, 0, st, "rotation", p);
 }
 
 // ---------------------------------------------------------------- failure-detection self-tests
@@ -942,7 +1043,8 @@ int llama_attn_decode_noalloc(const void* q, const void* k_cache, const void* v_
 size_t llama_attn_decode_prefix_workspace_bytes(int bsz, int n_heads, int n_kv_heads,
                                                 int prefix_len, int head_dim) {
   if (bsz < 1 || n_heads < 1 || n_kv_heads < 1 || prefix_len < 0 || head_dim < 1) return 0;
-  return 256;
+  if (n_heads % n_kv_heads != 0) return 0;
+  return prefix_layout(bsz, n_heads, n_kv_heads, prefix_len, head_dim).bytes;
 }
 
 int llama_attn_decode_prefix(const void* q, const void* k_new, const void* v_new,
@@ -968,35 +1070,23 @@ int llama_attn_decode_prefix(const void* q, const void* k_new, const void* v_new
   const long long* vs = v_prefix_strides ? v_prefix_strides : dense;
   if (prefix_len > 0)
     for (int i = 0; i < 2; ++i)
-      if (ks[i] % 8 || vs[i] % 8 || ks[i] < head_dim || vs[i] < head_dim)
+      if (ks[i] % 8 || vs[i] % 8 || ks[i] < head_dim || vs[i] < head_dim ||
+          ks[i] >= kMaxPrefixStride || vs[i] >= kMaxPrefixStride)
         return LLAMA_ERR_INVALID_ARG;
+  if (static_cast<long long>(bsz) * n_heads > 0x7fffffffLL / 16) return LLAMA_ERR_INVALID_ARG;
   if (dtype != LLAMA_DT_BF16) return LLAMA_ERR_UNSUPPORTED;
   if (bsz > la::dec::MAX_BATCH) return LLAMA_ERR_UNSUPPORTED;
   const size_t need = llama_attn_decode_prefix_workspace_bytes(bsz, n_heads, n_kv_heads, prefix_len,
                                                                head_dim);
   if (workspace == nullptr || workspace_bytes < need) return LLAMA_ERR_INVALID_ARG;
-  la::DecodePrefixParams p;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k_pre = static_cast<const __nv_bfloat16*>(k_prefix);
-  p.v_pre = static_cast<const __nv_bfloat16*>(v_prefix);
-  p.kp_head = ks[0], p.kp_row = ks[1], p.vp_head = vs[0], p.vp_row = vs[1];
-  p.k_new = static_cast<const __nv_bfloat16*>(k_new);
-  p.v_new = static_cast<const __nv_bfloat16*>(v_new);
-  p.k_cache = static_cast<__nv_bfloat16*>(k_cache);
-  p.v_cache = static_cast<__nv_bfloat16*>(v_cache);
-  p.lens = cache_lens;
-  p.out = static_cast<__nv_bfloat16*>(out);
-  p.prefix_len = prefix_len;
-  p.H = n_heads;
-  p.Hkv = n_kv_heads;
-  p.L = max_cache_len;
-  p.group = n_heads / n_kv_heads;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  const dim3 grid(n_heads, bsz);
   cudaStream_t st = as_stream(cuda_stream);
-  if (head_dim == 128) la::decode_prefix_plain_kernel<128><<<grid, 128, 0, st>>>(p);
-  else la::decode_prefix_plain_kernel<64><<<grid, 128, 0, st>>>(p);
-  return launch_status();
+  if (head_dim == 128)
+    return decode_prefix<128>(q, k_new, v_new, k_prefix, v_prefix, prefix_len, ks, vs, k_cache,
+                              v_cache, cache_lens, bsz, n_heads, n_kv_heads, max_cache_len, scale,
+                              out, workspace, st);
+  return decode_prefix<64>(q, k_new, v_new, k_prefix, v_prefix, prefix_len, ks, vs, k_cache, v_cache,
+                           cache_lens, bsz, n_heads, n_kv_heads, max_cache_len, scale, out,
+                           workspace, st);
 }
 
 int llama_attn_selftest_wait_timeout(unsigned int limit_us, void* cuda_stream) {
