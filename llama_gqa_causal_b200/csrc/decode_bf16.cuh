@@ -155,54 +155,72 @@ __device__ __forceinline__ long long share_owner(long long x, long long n, long 
   return ((x + 1) * g + n - 1) / n - 1;
 }
 
-// Chunk counts per batch entry, prefix-summed (identical in every CTA): each
-// thread sums a contiguous run of entries, the run totals are scanned with
-// warp shuffles and the per-warp totals, then each thread writes the prefixes
-// of its run.  chunk_prefix is shared memory of bsz + 1 entries; every thread
-// of a block of NTHREADS takes part.
-template <bool APPEND, int NTHREADS>
-__device__ __forceinline__ void scan_chunks(int* chunk_prefix, const DecodeParams& p) {
-  using namespace dec;
-  __shared__ int warp_total[NTHREADS / 32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = (p.bsz + NTHREADS - 1) / NTHREADS;
-  const int lo = min(p.bsz, static_cast<int>(threadIdx.x) * per), hi = min(p.bsz, lo + per);
-  int sum = 0;
-  for (int b = lo; b < hi; ++b) sum += (attend_len(p.lens[b], p.L, APPEND) + CH - 1) / CH;
-  int incl = sum;  // inclusive scan of the run totals within the warp
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) warp_total[warp] = incl;
-  __syncthreads();
-  int acc = incl - sum;  // exclusive prefix of this thread's run
-  for (int w = 0; w < warp; ++w) acc += warp_total[w];
-  if (threadIdx.x == NTHREADS - 1) chunk_prefix[p.bsz] = acc + sum;
-  for (int b = lo; b < hi; ++b) {
-    chunk_prefix[b] = acc;
-    acc += (attend_len(p.lens[b], p.L, APPEND) + CH - 1) / CH;
-  }
-  __syncthreads();
-}
-
-// One CTA's share of the chunks: CTA `cta` of n_ctas.  The first NCW + 1 warps
-// of the block take part (NCW consumers, then the producer); s.chunk_prefix is
-// filled in and the barriers of s are initialised.
 template <int D, bool APPEND>
-__device__ __forceinline__ void decode_share(DecSmem<D>& s, const CUtensorMap& tm_k,
-                                             const CUtensorMap& tm_v, const DecodeParams& p,
-                                             int cta, int n_ctas) {
+__global__ void __launch_bounds__(dec::THREADS, 1) decode_bf16_kernel(
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    DecodeParams p) {
   using namespace dec;
   constexpr int KSTEPS = D / 16;  // k-steps of the QK^T product, m-tiles of PV
   constexpr int CB = D / 64;      // 64-column swizzle blocks per row
   constexpr uint32_t STAGE_BLOCK_BYTES = TR * 64 * 2;  // one [64 rows x 64 cols] block
+  extern __shared__ uint8_t smem_raw[];
+  DecSmem<D>& s = *reinterpret_cast<DecSmem<D>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per_b = p.Hkv * p.hchunks;  // sequences per batch entry
+  if (warp == NCW && elect_one()) {  // descriptor fetch overlaps the prologue
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (threadIdx.x == 0) {  // shared memory only: set up before the grid-dependency wait
+    for (int i = 0; i < NSTAGE; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], NCW);
+    }
+    fence_mbar_init();
+  }
+  // Launched as a programmatic dependent of whatever precedes it on the stream:
+  // the CTAs may be resident before that grid has finished, so nothing in
+  // global memory is read or written before this wait (the previous decode's
+  // combine still reads the workspace this kernel writes).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // ---- chunk counts per batch entry, prefix-summed (identical in every CTA):
+  // each thread sums a contiguous run of entries, the run totals are scanned
+  // with warp shuffles and the per-warp totals, then each thread writes the
+  // prefixes of its run
+  {
+    __shared__ int warp_total[THREADS / 32];
+    const int per = (p.bsz + THREADS - 1) / THREADS;
+    const int lo = min(p.bsz, static_cast<int>(threadIdx.x) * per), hi = min(p.bsz, lo + per);
+    int sum = 0;
+    for (int b = lo; b < hi; ++b) sum += (attend_len(p.lens[b], p.L, APPEND) + CH - 1) / CH;
+    int incl = sum;  // inclusive scan of the run totals within the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_total[warp] = incl;
+    __syncthreads();
+    int acc = incl - sum;  // exclusive prefix of this thread's run
+    for (int w = 0; w < warp; ++w) acc += warp_total[w];
+    if (threadIdx.x == THREADS - 1) s.chunk_prefix[p.bsz] = acc + sum;
+    for (int b = lo; b < hi; ++b) {
+      s.chunk_prefix[b] = acc;
+      acc += (attend_len(p.lens[b], p.L, APPEND) + CH - 1) / CH;
+    }
+    __syncthreads();
+    // the combine kernel reads the prefix once this grid has finished
+    if (blockIdx.x == 0)
+      for (int b = threadIdx.x; b <= p.bsz; b += THREADS) p.ws_prefix[b] = s.chunk_prefix[b];
+  }
+  // the combine kernel may be scheduled now; it waits for this grid to finish
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long n_chunks = static_cast<long long>(s.chunk_prefix[p.bsz]) * per_b;
-  const long long x0 = share_start(cta, n_chunks, n_ctas);
-  const long long x1 = share_start(cta + 1, n_chunks, n_ctas);
+  const long long x0 = share_start(blockIdx.x, n_chunks, gridDim.x);
+  const long long x1 = share_start(blockIdx.x + 1, n_chunks, gridDim.x);
   if (x0 >= x1) return;  // uniform across the CTA: no share
 
   if (warp == NCW) {  // ---------------------------------------------- TMA producer
@@ -487,7 +505,7 @@ __device__ __forceinline__ void decode_share(DecSmem<D>& s, const CUtensorMap& t
           const int head = m.kvh * p.group + m.hc * 8 + hh;
           float* dst = m.home
               ? p.ws_home + (static_cast<size_t>(m.b) * p.H + head) * part_stride(D)
-              : p.ws_cta + (static_cast<size_t>(cta) * 8 + hh) * part_stride(D);
+              : p.ws_cta + (static_cast<size_t>(blockIdx.x) * 8 + hh) * part_stride(D);
 #pragma unroll
           for (int i = 0; i < PER; i += 4) {
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -510,42 +528,6 @@ __device__ __forceinline__ void decode_share(DecSmem<D>& s, const CUtensorMap& t
     }
     if (m.last) break;
   }
-}
-
-template <int D, bool APPEND>
-__global__ void __launch_bounds__(dec::THREADS, 1) decode_bf16_kernel(
-    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-    DecodeParams p) {
-  using namespace dec;
-  extern __shared__ uint8_t smem_raw[];
-  DecSmem<D>& s = *reinterpret_cast<DecSmem<D>*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-
-  const int warp = threadIdx.x >> 5;
-  if (warp == NCW && elect_one()) {  // descriptor fetch overlaps the prologue
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
-  }
-  if (threadIdx.x == 0) {  // shared memory only: set up before the grid-dependency wait
-    for (int i = 0; i < NSTAGE; ++i) {
-      mbar_init(&s.full[i], 1);
-      mbar_init(&s.empty[i], NCW);
-    }
-    fence_mbar_init();
-  }
-  // Launched as a programmatic dependent of whatever precedes it on the stream:
-  // the CTAs may be resident before that grid has finished, so nothing in
-  // global memory is read or written before this wait (the previous decode's
-  // combine still reads the workspace this kernel writes).
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-
-  scan_chunks<APPEND, THREADS>(s.chunk_prefix, p);
-  // the combine kernel reads the prefix once this grid has finished
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b <= p.bsz; b += THREADS) p.ws_prefix[b] = s.chunk_prefix[b];
-  // the combine kernel may be scheduled now; it waits for this grid to finish
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  decode_share<D, APPEND>(s, tm_k, tm_v, p, blockIdx.x, gridDim.x);
 }
 
 // Merge the partials of the heads of one sequence (batch entry, K/V head,

@@ -5,7 +5,8 @@
 // the same prefix, so that part is a product of matrices and runs on tcgen05:
 //   S = Q K_prefix^T (128 query rows x 128 keys), P = 2^(S c - m), O += P V_prefix
 // with each prefix tile read once for up to 256 query rows.  The sequences' own
-// rows are read once each by decode_share, the split-KV decode.  Both parts run
+// rows are a separate stream of 16-row tiles for mma.sync (own_share), as in
+// the split-KV decode but with every warp a worker of its own.  Both parts run
 // in one launch of one CTA per SM: the CTAs are dealt out on the device, in
 // proportion to the two parts' work (cache_lens is known only there), because
 // the prefix part is bound by exponentials and products as soon as a few rows
@@ -48,27 +49,40 @@ static_assert(kRegsControl + 2 * kRegsSoftmax <= 3 * kRegsAtLaunch,
               "setmaxnreg split exceeds the registers the block is launched with");
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int kPolyPairsOf8 = 3;  // pairs of 8 exponentiated on the FMA pipe
-// Work of an item and of a 64-row chunk of a cache, in units that only their
+// Work of an item and of a 16-row tile of a cache, in units that only their
 // ratios matter of: what one SM takes for it.
 __host__ __device__ constexpr float cost_pair(int d) { return d == 128 ? 2.1f : 1.5f; }
 __host__ __device__ constexpr float cost_single(int d) { return d == 128 ? 1.2f : 0.8f; }
-__host__ __device__ constexpr float cost_chunk(int d) { return d == 128 ? 0.55f : 0.35f; }
+__host__ __device__ constexpr float cost_tile(int d) { return d == 128 ? 0.12f : 0.07f; }
+__host__ __device__ constexpr float cost_head() { return 5.f; }
 // Floats of one unit's partial: [D + 2][BM], the outputs of a row down a
 // column, then its maximum and sum (lanes are rows, so both the writing warp
 // and the combining one touch whole lines).
 __host__ __device__ constexpr int unit_floats(int d) { return (d + 2) * BM; }
-constexpr int HDR = 4;  // ints before the chunk prefix: groups, CTAs of a group, own CTAs
+// Own rows: warps of a CTA, stages of a warp, rows of a tile.
+constexpr int OW = THREADS / 32;
+constexpr int OS = 2;
+constexpr int OT = 16;
 }  // namespace px
 
 struct PrefixParams {
   const __nv_bfloat16* q;  // [b, H, D]
-  float* part;             // [tile pairs * Hkv + MAX_CTAS][2][D + 2][BM]
-  int* hdr;                // [HDR + b + 1]
+  float* part;             // prefix partials [tile pairs * Hkv + MAX_CTAS][2][D + 2][BM]
+  float* own_home;         // [b, H, D + 4]: an own segment from its sequence's first row
+  float* own_mid;          // [MAX_CTAS * OW][8, D + 4]: a worker's segment from inside one
+  int2* part_of;           // [tile pairs * Hkv] CTA with the home slot, segments
+  int2* own_of;            // [b * Hkv * hchunks] worker with the home slot, segments
   int rows;                // query rows of a K/V head: b * group
-  int P;                   // keys
-  int nt;                  // key tiles
+  int P;                   // keys of the prefix
+  int nt;                  // its key tiles
   int pairs;               // tile pairs: ceil(rows / 256)
-  int H, Hkv, group;
+  int b, H, Hkv, L, group;
+  int hchunks;             // ceil(group / 8)
+  const int* lens;             // [b]
+  const __nv_bfloat16* k_new;  // [b, Hkv, D] or null
+  const __nv_bfloat16* v_new;
+  __nv_bfloat16* k_cache;      // [b, Hkv, L, D]
+  __nv_bfloat16* v_cache;
   float scale_log2;
 };
 
@@ -79,27 +93,31 @@ struct PrefixParams {
 struct PrefixPlan {
   int groups, per, own;
 };
-__device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams& x, long long n_chunks,
-                                                  int n_ctas, float c_pair, float c_single,
-                                                  float c_chunk) {
+__device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams& x, int n_tiles, int n_ctas,
+                                                  float c_pair, float c_single, float c_tile) {
   PrefixPlan r = {0, 0, 0};
-  const long long items = static_cast<long long>(x.Hkv) * x.nt;  // of one tile pair
+  const int items = x.Hkv * x.nt;  // of one tile pair
   if (items > 0) {
     const bool single = x.rows - (x.pairs - 1) * 2 * px::BM <= px::BM;  // the last pair
     const float wa = static_cast<float>(items) *
                      (static_cast<float>(x.pairs - single) * c_pair + (single ? c_single : 0.f));
-    const float wb = static_cast<float>(n_chunks) * c_chunk;
-    int na = static_cast<int>(static_cast<float>(n_ctas) * wa / (wa + wb) + 0.5f);
-    na = max(1, min(na, n_chunks > 0 ? n_ctas - 1 : n_ctas));
+    const float wb = static_cast<float>(n_tiles) * c_tile;
+    // na with head + wa / na = wb / (n - na), where head is what a prefix CTA
+    // takes besides its items
+    const float n = static_cast<float>(n_ctas), h = px::cost_head();
+    const float p = wa + wb - h * n;
+    int na = n_tiles == 0 ? n_ctas
+                          : static_cast<int>((sqrtf(p * p + 4.f * h * wa * n) - p) / (2.f * h) + 0.5f);
+    na = max(1, min(na, n_tiles > 0 ? n_ctas - 1 : n_ctas));
     if (x.pairs <= na && (na / x.pairs) * x.pairs * 8 >= na * 7) {
       r.groups = x.pairs;
-      r.per = static_cast<int>(min(static_cast<long long>(na / x.pairs), items));
+      r.per = min(na / x.pairs, items);
     } else {
       r.groups = 1;
-      r.per = static_cast<int>(min(static_cast<long long>(na), items * x.pairs));
+      r.per = min(na, items * x.pairs);
     }
   }
-  r.own = static_cast<int>(min(n_chunks, static_cast<long long>(n_ctas - r.groups * r.per)));
+  r.own = min(n_tiles, n_ctas - r.groups * r.per);
   return r;
 }
 
@@ -146,13 +164,11 @@ struct PrefixSegment {
   int j0, n;      // key tiles
   bool single;    // both units on the same rows, key tiles in turn
 };
-__device__ __forceinline__ PrefixSegment prefix_segment(const PrefixParams& x, long long i0,
-                                                        long long i1) {
+__device__ __forceinline__ PrefixSegment prefix_segment(const PrefixParams& x, int i0, int i1) {
   PrefixSegment g;
-  const long long seq = i0 / x.nt;
-  g.seq = static_cast<int>(seq);
-  g.j0 = static_cast<int>(i0 - seq * x.nt);
-  g.n = static_cast<int>(min(static_cast<long long>(x.nt - g.j0), i1 - i0));
+  g.seq = i0 / x.nt;
+  g.j0 = i0 - g.seq * x.nt;
+  g.n = min(x.nt - g.j0, i1 - i0);
   const int pair = g.seq / x.Hkv;
   g.kvh = g.seq - pair * x.Hkv;
   g.row0 = pair * 2 * px::BM;
@@ -161,11 +177,11 @@ __device__ __forceinline__ PrefixSegment prefix_segment(const PrefixParams& x, l
   return g;
 }
 
-// The items [x0, x1) by one CTA.
+// One prefix CTA's run of items.
 template <int D>
 __device__ __forceinline__ void prefix_share(PrefixSmem<D>& s, const CUtensorMap& tm_k,
                                              const CUtensorMap& tm_v, const PrefixParams& x,
-                                             int cta, long long x0, long long x1) {
+                                             const PrefixPlan& plan, int cta) {
   using namespace px;
   constexpr int CB = D / 64;                  // 64-column swizzle blocks per row
   constexpr int NST = ring(D);
@@ -175,27 +191,78 @@ __device__ __forceinline__ void prefix_share(PrefixSmem<D>& s, const CUtensorMap
   constexpr uint32_t IDESC_PV = idesc_bf16(BM, D, true);
   constexpr uint32_t TMEM_COLS = 512;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int items = x.Hkv * x.nt * (x.pairs / plan.groups);  // of this CTA's group
+  const int group = cta / plan.per, in_group = cta - group * plan.per;
+  const int x0 = group * items + static_cast<int>(share_start(in_group, items, plan.per));
+  const int x1 = group * items + static_cast<int>(share_start(in_group + 1, items, plan.per));
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < NST; ++i) {
-      mbar_init(&s.full[i], 1);
-      mbar_init(&s.empty[i], 1);
+  // ---- Q rows into a unit's tile, by its softmax warps: row m of the K/V head
+  // is batch entry m / group, head kvh * group + m % group; a row's 16-byte
+  // chunks go to adjacent lanes.  Rows past the end are zero.
+  auto stage_q = [&](const PrefixSegment& g, int t) {
+    constexpr int CH16 = D / 8;
+    constexpr int RPS = 32 / CH16;
+    const int r0 = (warp & 3) * 32 + lane / CH16, c = lane % CH16;
+    const int rows = min(BM, g.rows - t * BM);
+    // one division a call: the rows that follow are reached by adding
+    const int m = g.row0 + t * BM + r0;
+    const int b = m / x.group;
+    int h = m - b * x.group;
+    const __nv_bfloat16* src =
+        x.q + (static_cast<size_t>(b) * x.H + g.kvh * x.group + h) * D + c * 8;
+    const int h_step = RPS % x.group;
+    const long long jump = static_cast<long long>(x.H - x.group) * D;  // to the next entry's heads
+    const long long step = static_cast<long long>(RPS) * D + (RPS / x.group) * jump;
+    uint4 v[32 / RPS];
+#pragma unroll
+    for (int st = 0; st < 32 / RPS; ++st) {
+      v[st] = r0 + st * RPS < rows ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
+      src += step;
+      h += h_step;
+      if (h >= x.group) {
+        h -= x.group;
+        src += jump;
+      }
     }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(&s.q_ready[t], 4);
-      mbar_init(&s.s_full[t], 1);
-      mbar_init(&s.p_lo[t], 4);
-      mbar_init(&s.p_hi[t], 4);
-      mbar_init(&s.o_full[t], 1);
+    uint8_t* qs = reinterpret_cast<uint8_t*>(&s.q[t][0]) + (c / 8) * BLOCK_BYTES;
+#pragma unroll
+    for (int st = 0; st < 32 / RPS; ++st)
+      *reinterpret_cast<uint4*>(qs + sw128_offset(r0 + st * RPS, c % 8)) = v[st];
+    fence_proxy_async_smem();
+  };
+  // ---- setup, with the first loads on their way: Q, and the first K tile (the
+  // rest of the ring follows the sync, so that Q does not queue behind it)
+  if (warp == 0) {
+    if (elect_one()) {
+      for (int i = 0; i < NST; ++i) {
+        mbar_init(&s.full[i], 1);
+        mbar_init(&s.empty[i], 1);
+      }
+      for (int t = 0; t < 2; ++t) {
+        mbar_init(&s.q_ready[t], 4);
+        mbar_init(&s.s_full[t], 1);
+        mbar_init(&s.p_lo[t], 4);
+        mbar_init(&s.p_hi[t], 4);
+        mbar_init(&s.o_full[t], 1);
+      }
+      mbar_init(&s.mma_done, 1);
+      fence_mbar_init();
+      const PrefixSegment g = prefix_segment(x, x0, x1);
+      mbar_arrive_expect_tx(&s.full[0], TILE_BYTES);
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb)
+        tma_load_3d(reinterpret_cast<uint8_t*>(&s.ring[0][0]) + cb * BLOCK_BYTES, &tm_k, &s.full[0],
+                    cb * 64, g.j0 * BN, g.kvh);
     }
-    mbar_init(&s.mma_done, 1);
-    fence_mbar_init();
-  }
-  if (warp == 1) {
+    __syncwarp();
+  } else if (warp == 1) {
     tmem_alloc(&s.tmem_base, TMEM_COLS);
     tmem_relinquish();
+  } else if (warp >= 4) {
+    const PrefixSegment g = prefix_segment(x, x0, x1);
+    const int t = (warp - 4) >> 2;
+    if (!g.single || t == 0) stage_q(g, t);
   }
-  fence_proxy_async_smem();  // the chunk scan wrote where the ring's copies land
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -208,12 +275,7 @@ __device__ __forceinline__ void prefix_share(PrefixSmem<D>& s, const CUtensorMap
     // Tiles in the order of their use: of a segment K_0 (and K_1 if the units
     // take the tiles in turn), then V_j and the K tile that follows the ones sent.
     setmaxnreg_dec<kRegsControl>();
-    if (elect_one()) {
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-    }
-    __syncwarp();
-    uint32_t sent = 0;  // tiles put into the ring
+    uint32_t sent = 1;  // tiles put into the ring
     bool ok = true;
     auto send = [&](const CUtensorMap* m, int kvh, int j) {
       const int st = static_cast<int>(sent % NST);
@@ -231,11 +293,11 @@ __device__ __forceinline__ void prefix_share(PrefixSmem<D>& s, const CUtensorMap
       __syncwarp();
       ++sent;
     };
-    for (long long i = x0; i < x1 && ok;) {
+    for (int i = x0; i < x1 && ok;) {
       const PrefixSegment g = prefix_segment(x, i, x1);
       i += g.n;
       const int ahead = g.single ? 2 : 1;
-      send(&tm_k, g.kvh, g.j0);
+      if (i > x0 + g.n) send(&tm_k, g.kvh, g.j0);  // (the very first is on its way)
       if (g.single && g.n > 1 && ok) send(&tm_k, g.kvh, g.j0 + 1);
       for (int j = 0; j < g.n && ok; ++j) {
         send(&tm_v, g.kvh, g.j0 + j);
@@ -278,83 +340,62 @@ __device__ __forceinline__ void prefix_share(PrefixSmem<D>& s, const CUtensorMap
       if (elect_one()) tc_commit(bar);
       __syncwarp();
     };
-    uint32_t used = 0;  // tiles taken from the ring
-    uint32_t cnt[2] = {0, 0};  // P tiles of each unit so far
-    uint32_t seg = 0;
-    bool ok = true;
-    auto wait_tile = [&](uint32_t i) {
-      ok = mbar_wait(&s.full[i % NST], (i / NST) & 1);
-      if (ok) tc_fence_after();
-      return ok;
-    };
-    auto half = [&](int t, int st, bool accumulate, int h) {
-      if (!mbar_wait(h ? &s.p_hi[t] : &s.p_lo[t], cnt[t] & 1)) return false;
+    // the ring: the next tile to be taken, and the parity of its full barrier
+    int next_st = 0;
+    uint32_t next_ph = 0;
+    auto take = [&](int& st) {
+      st = next_st;
+      if (!mbar_wait(&s.full[st], next_ph)) return false;
       tc_fence_after();
-      issue_pv(t, st, accumulate, h);
+      if (++next_st == NST) {
+        next_st = 0;
+        next_ph ^= 1;
+      }
       return true;
     };
-    for (long long i = x0; i < x1 && ok; ++seg) {
+    uint32_t cnt0 = 0, cnt1 = 0;  // P tiles of each unit so far
+    uint32_t seg = 0;
+    bool ok = true;
+    for (int i = x0; i < x1 && ok; ++seg) {
       const PrefixSegment g = prefix_segment(x, i, x1);
       i += g.n;
       ok = mbar_wait(&s.q_ready[0], seg & 1) && mbar_wait(&s.q_ready[1], seg & 1);
-      if (!ok || !wait_tile(used)) break;
-      if (g.single) {
-        issue_qk(0, 0, static_cast<int>(used % NST));
-        commit(&s.empty[used % NST]);
-        ++used;
-        if (g.n > 1) {
-          if (!wait_tile(used)) break;
-          issue_qk(1, 0, static_cast<int>(used % NST));
-          commit(&s.empty[used % NST]);
-          ++used;
-        }
-        for (int j = 0; j < g.n; ++j) {
-          const int t = j & 1;
-          const int vs = static_cast<int>(used % NST);
-          if (!wait_tile(used)) break;
-          ++used;
-          ok = half(t, vs, j > 1, 0) && half(t, vs, true, 1);
-          if (!ok) break;
-          ++cnt[t];
-          commit(&s.empty[vs]);
-          if (j + 2 < g.n) {
-            if (!wait_tile(used)) break;
-            issue_qk(t, 0, static_cast<int>(used % NST));
-            commit(&s.empty[used % NST]);
-            ++used;
-          } else {
-            commit(&s.o_full[t]);
+      // step u of a segment is unit u & 1's, whether the units share the key
+      // tiles (two steps a tile) or take them in turn
+      const int steps = g.single ? g.n : 2 * g.n;
+      int vs = 0, ks = 0;
+#pragma unroll 1
+      for (int u = -2; u < steps && ok; ++u) {
+        const int t = u & 1;
+        if (u >= 0) {  // O_t += P_t V
+          if ((g.single || t == 0) && !take(vs)) {
+            ok = false;
+            break;
           }
-        }
-        // (a unit without a tile waits here all the same: running ahead, it would
-        // complete two phases of q_ready between two of this warp's waits)
-        if (ok && g.n == 1) commit(&s.o_full[1]);
-      } else {
-        issue_qk(0, 0, static_cast<int>(used % NST));
-        issue_qk(1, 1, static_cast<int>(used % NST));
-        commit(&s.empty[used % NST]);
-        ++used;
-        for (int j = 0; j < g.n && ok; ++j) {
-          const bool next = j + 1 < g.n;
-          const int vs = static_cast<int>(used % NST);
-          const uint32_t kn = used + 1;
-          if (!wait_tile(used)) break;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            ok = half(t, vs, j > 0, 0) && half(t, vs, true, 1);
+          const uint32_t ph = (t ? cnt1 : cnt0) & 1;
+          if (t) ++cnt1;
+          else ++cnt0;
+#pragma unroll 1
+          for (int h = 0; h < 2 && ok; ++h) {
+            ok = mbar_wait(h ? &s.p_hi[t] : &s.p_lo[t], ph);
             if (!ok) break;
-            ++cnt[t];
-            if (next) {
-              if (t == 0 && !wait_tile(kn)) break;
-              issue_qk(t, t, static_cast<int>(kn % NST));
-            } else {
-              commit(&s.o_full[t]);
-            }
+            tc_fence_after();
+            issue_pv(t, vs, u > 1 || h > 0, h);
           }
           if (!ok) break;
-          commit(&s.empty[vs]);
-          if (next) commit(&s.empty[kn % NST]);
-          used = next ? kn + 1 : kn;
+          if (g.single || t == 1) commit(&s.empty[vs]);
+        }
+        if (u + 2 < steps) {  // S_t = Q K^T of the unit's next tile
+          if ((g.single || t == 0) && !take(ks)) {
+            ok = false;
+            break;
+          }
+          issue_qk(t, g.single ? 0 : t, ks);
+          if (g.single || t == 1) commit(&s.empty[ks]);
+        } else {
+          // (a unit without a tile waits for this all the same: running ahead, it
+          // would complete two phases of q_ready between two of this warp's waits)
+          commit(&s.o_full[t]);
         }
       }
     }
@@ -362,7 +403,33 @@ __device__ __forceinline__ void prefix_share(PrefixSmem<D>& s, const CUtensorMap
     commit(&s.mma_done);
     mbar_wait(&s.mma_done, 0);
   } else if (warp < 4) {
-    setmaxnreg_dec<kRegsControl>();  // idle warps of warpgroup 0
+    setmaxnreg_dec<kRegsControl>();
+    // warp 2 notes where the combine kernel finds the segments of every (tile
+    // pair, K/V head) that starts here; warp 3 brings the later segments' Q to L2
+    if (warp == 3)
+      for (int i = x0; i < x1;) {
+        const PrefixSegment g = prefix_segment(x, i, x1);
+        if (i > x0)
+          for (int rr = lane; rr < g.rows; rr += 32) {
+            const int m = g.row0 + rr;
+            const int b = m / x.group, h = m - b * x.group;
+            const __nv_bfloat16* row =
+                x.q + (static_cast<size_t>(b) * x.H + g.kvh * x.group + h) * D;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(row));
+            if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 64));
+          }
+        i += g.n;
+      }
+    if (warp == 2 && lane == 0)
+      for (int i = x0; i < x1;) {
+        const PrefixSegment g = prefix_segment(x, i, x1);
+        if (g.j0 == 0) {
+          const int end = i + x.nt - 1 - group * items;
+          x.part_of[g.seq] = make_int2(
+              cta, group * plan.per + static_cast<int>(share_owner(end, items, plan.per)) - cta + 1);
+        }
+        i += g.n;
+      }
   } else {
     // ================================================================ softmax
     setmaxnreg_inc<kRegsSoftmax>();
@@ -375,46 +442,17 @@ __device__ __forceinline__ void prefix_share(PrefixSmem<D>& s, const CUtensorMap
     const bool scale_pos = c_log2 > 0.f;
     uint32_t sc = 0, oc = 0;  // S tiles and finished segments of this unit so far
     bool ok = true;
-    for (long long i = x0; i < x1 && ok;) {
+    if (lane == 0) mbar_arrive(&s.q_ready[t]);
+#pragma unroll 1
+    for (int i = x0; i < x1;) {
       const PrefixSegment g = prefix_segment(x, i, x1);
       i += g.n;
-      const int tq = g.single ? 0 : t;
-      const int rows = min(BM, g.rows - tq * BM);  // of this unit
-      const bool active = quarter * 32 < rows;     // (warps past the rows only keep step)
-      // ---- Q rows into the unit's tile: row m of the K/V head is batch entry
-      // m / group, head kvh * group + m % group; a row's 16-byte chunks go to
-      // adjacent lanes.  Rows past the end are zero.
-      if (tq == t) {
-        constexpr int CH16 = D / 8;
-        constexpr int RPS = 32 / CH16;
-        uint4 v[32 / RPS];
-#pragma unroll
-        for (int st = 0; st < 32 / RPS; ++st) {
-          const int rr = quarter * 32 + st * RPS + lane / CH16;
-          v[st] = make_uint4(0, 0, 0, 0);
-          if (rr < rows) {
-            const int m = g.row0 + tq * BM + rr;
-            const int b = m / x.group, h = m - b * x.group;
-            v[st] = *reinterpret_cast<const uint4*>(
-                x.q + (static_cast<size_t>(b) * x.H + g.kvh * x.group + h) * D + (lane % CH16) * 8);
-          }
-        }
-        uint8_t* qs = reinterpret_cast<uint8_t*>(&s.q[t][0]);
-#pragma unroll
-        for (int st = 0; st < 32 / RPS; ++st) {
-          const int rr = quarter * 32 + st * RPS + lane / CH16;
-          const int c = lane % CH16;
-          *reinterpret_cast<uint4*>(qs + (c / 8) * BLOCK_BYTES + sw128_offset(rr, c % 8)) = v[st];
-        }
-        fence_proxy_async_smem();
-      }
-      tc_fence_before();  // (the last segment's O has been read)
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.q_ready[t]);
-
+      const int rows = min(BM, g.rows - (g.single ? 0 : t) * BM);  // of this unit
+      const bool active = quarter * 32 < rows;  // (warps past the rows only keep step)
       float m_ref = -INFINITY;  // reference maximum (log2 units) of the exponentials
       float l_sum = 0.f;
       const int n_mine = g.single ? (g.n + 1 - t) / 2 : g.n;
+#pragma unroll 1
       for (int jj = 0; jj < n_mine; ++jj) {
         const int j = g.j0 + (g.single ? 2 * jj + t : jj);
         if (!mbar_wait(&s.s_full[t], sc & 1)) { ok = false; break; }
@@ -536,9 +574,20 @@ __device__ __forceinline__ void prefix_share(PrefixSmem<D>& s, const CUtensorMap
       float* dst = x.part + (static_cast<size_t>(slot) * 2 + t) * unit_floats(D) + r;
       if (!mbar_wait(&s.o_full[t], oc & 1)) break;
       ++oc;
+      // the next segment's Q first: its scores are taken while O is written out
+      // (which no product touches before this unit's next P)
+      if (i < x1) {
+        const PrefixSegment next = prefix_segment(x, i, x1);
+        if (!next.single || t == 0) stage_q(next, t);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.q_ready[t]);
+      }
       tc_fence_after();
-      if (active && n_mine > 0) {
-#pragma unroll
+      if (n_mine == 0) {  // (no tile: O is not this segment's)
+        if (r < rows)
+          for (int e = 0; e < D; ++e) dst[e * BM] = 0.f;
+      } else if (active) {
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t orr[32];
           tmem_ld32(my_o + c * 32, orr);
@@ -565,9 +614,262 @@ __device__ __forceinline__ void prefix_share(PrefixSmem<D>& s, const CUtensorMap
   }
 }
 
+// The sequences' own rows.  A sequence here is (batch entry, K/V head, chunk of
+// up to 8 query heads); its rows are cut into tiles of 16, the tiles of all
+// sequences are numbered through, and every warp of every own CTA takes an even
+// share of them.  A warp feeds itself (its own ring of tiles, one lane issuing
+// the copies) and keeps the running softmax of its 16 keys x 8 heads in
+// registers, so no warp waits for another: with four warps of a block sharing
+// 64-row tiles and merging at the end of every sequence, 1024 sequences of 256
+// rows ran at 2.7 TB/s.
+//   S^T[16 keys x 8 heads]  = K[16 x D] . Q^T[D x 8]
+//   O^T[D x 8 heads]       += V^T[D x 16] . P^T[16 x 8]
+template <int D>
+struct OwnSmem {
+  alignas(1024) __nv_bfloat16 k[px::OW][px::OS][px::OT * D];
+  alignas(1024) __nv_bfloat16 v[px::OW][px::OS][px::OT * D];
+  uint64_t full[px::OW][px::OS];
+  int before[dec::MAX_BATCH + 1];  // tiles of a head chunk's sequences in the entries before b
+};
+
+// before[b] = tiles of one sequence of each of the entries 0 .. b - 1, summed;
+// every thread of the block takes part.
+template <bool APPEND>
+__device__ __forceinline__ void scan_tiles(int* before, const PrefixParams& x) {
+  using namespace px;
+  __shared__ int warp_total[THREADS / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = (x.b + THREADS - 1) / THREADS;
+  const int lo = min(x.b, static_cast<int>(threadIdx.x) * per), hi = min(x.b, lo + per);
+  int sum = 0;
+  for (int b = lo; b < hi; ++b) sum += (attend_len(x.lens[b], x.L, APPEND) + OT - 1) / OT;
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) warp_total[warp] = incl;
+  __syncthreads();
+  int acc = incl - sum;
+  for (int w = 0; w < warp; ++w) acc += warp_total[w];
+  if (threadIdx.x == THREADS - 1) before[x.b] = acc + sum;
+  for (int b = lo; b < hi; ++b) {
+    before[b] = acc;
+    acc += (attend_len(x.lens[b], x.L, APPEND) + OT - 1) / OT;
+  }
+  __syncthreads();
+}
+
+// A place in the list of tiles.
+struct OwnCursor {
+  int b, seq, c, n;  // batch entry, sequence within it, tile of that, its tiles
+};
+
+template <int D, bool APPEND>
+__device__ __forceinline__ void own_share(OwnSmem<D>& s, const CUtensorMap& tm_k,
+                                          const CUtensorMap& tm_v, const PrefixParams& x,
+                                          int worker, int n_workers, int n_tiles) {
+  using namespace px;
+  constexpr int KSTEPS = D / 16;
+  constexpr int CB = D / 64;
+  constexpr uint32_t BLOCK_BYTES = OT * 128;  // one [16 rows x 64 cols] block
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int mat = lane >> 3, r8 = lane & 7;
+  const int per_b = x.Hkv * x.hchunks;
+  const int x0 = static_cast<int>(share_start(worker, n_tiles, n_workers));
+  const int x1 = static_cast<int>(share_start(worker + 1, n_tiles, n_workers));
+
+  OwnCursor at;  // of the tile in hand
+  {
+    int lo = 0, hi = x.b - 1;  // the largest b with before[b] * per_b <= x0
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s.before[mid] * per_b <= x0) lo = mid;
+      else hi = mid - 1;
+    }
+    at.b = lo;
+    at.n = s.before[lo + 1] - s.before[lo];
+    const int rest = x0 - s.before[lo] * per_b;
+    at.seq = rest / at.n;
+    at.c = rest - at.seq * at.n;
+  }
+  OwnCursor to = at;  // of the next tile to be fetched
+  auto advance = [&](OwnCursor& u) {
+    if (++u.c < u.n) return;
+    u.c = 0;
+    if (++u.seq < per_b) return;
+    u.seq = 0;
+    do ++u.b;
+    while (u.b < x.b && s.before[u.b + 1] == s.before[u.b]);
+    u.n = u.b < x.b ? s.before[u.b + 1] - s.before[u.b] : 0;
+  };
+  auto fetch = [&](int i) {  // tile i of the list, at the cursor `to`
+    const int st = (i - x0) % OS;
+    if (elect_one()) {
+      mbar_arrive_expect_tx(&s.full[warp][st], 2u * OT * D * 2u);
+      const int bh = to.b * x.Hkv + to.seq / x.hchunks;
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) {
+        tma_load_3d(&s.k[warp][st][cb * OT * 64], &tm_k, &s.full[warp][st], cb * 64, to.c * OT, bh);
+        tma_load_3d(&s.v[warp][st][cb * OT * 64], &tm_v, &s.full[warp][st], cb * 64, to.c * OT, bh);
+      }
+    }
+    __syncwarp();
+    advance(to);
+  };
+  for (int i = x0; i < min(x0 + OS, x1); ++i) fetch(i);
+
+  uint32_t qf[KSTEPS][2];
+  float m_run[2], l_run[2], o[KSTEPS][4];
+  bool home = false;
+  int len = 0;
+  for (int i = x0; i < x1; ++i) {
+    const int st = (i - x0) % OS;
+    const int kvh = at.seq / x.hchunks, hc = at.seq - kvh * x.hchunks;
+    if (i == x0 || at.c == 0) {  // a segment starts
+      home = at.c == 0;
+      if (home) {
+        const int n = i + at.n <= x1 ? 1
+            : static_cast<int>(share_owner(i + at.n - 1, n_tiles, n_workers)) - worker + 1;
+        if (lane == 0) x.own_of[at.b * per_b + at.seq] = make_int2(worker, n);
+      }
+      len = attend_len(x.lens[at.b], x.L, APPEND);
+      // lane: head g of the chunk, dims kk * 16 + 2t + {0, 1, 8, 9}
+      const bool valid = hc * 8 + g < x.group;
+      const __nv_bfloat16* qr =
+          x.q + (static_cast<size_t>(at.b) * x.H + kvh * x.group + hc * 8 + g) * D + 2 * t;
+#pragma unroll
+      for (int kk = 0; kk < KSTEPS; ++kk) {
+        qf[kk][0] = valid ? *reinterpret_cast<const uint32_t*>(qr + kk * 16) : 0u;
+        qf[kk][1] = valid ? *reinterpret_cast<const uint32_t*>(qr + kk * 16 + 8) : 0u;
+      }
+      m_run[0] = m_run[1] = -INFINITY;
+      l_run[0] = l_run[1] = 0.f;
+#pragma unroll
+      for (int mt = 0; mt < KSTEPS; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
+    }
+    if (!mbar_wait(&s.full[warp][st], static_cast<uint32_t>((i - x0) / OS) & 1)) return;
+    const int n_valid = min(OT, len - at.c * OT);
+    uint8_t* kb = reinterpret_cast<uint8_t*>(&s.k[warp][st][0]);
+    uint8_t* vb = reinterpret_cast<uint8_t*>(&s.v[warp][st][0]);
+    const bool patch = APPEND && at.c == at.n - 1;  // the step's own row is the last
+    if (patch) {
+      const int r = n_valid - 1;
+      const size_t row = static_cast<size_t>(at.b) * x.Hkv + kvh;
+      const size_t crow = (row * x.L + (len - 1)) * D;
+      if (lane < D / 8) {
+        const uint4 kn = *reinterpret_cast<const uint4*>(x.k_new + row * D + lane * 8);
+        const uint4 vn = *reinterpret_cast<const uint4*>(x.v_new + row * D + lane * 8);
+        const uint32_t off = (lane / 8) * BLOCK_BYTES + sw128_offset(r, lane % 8);
+        *reinterpret_cast<uint4*>(kb + off) = kn;
+        *reinterpret_cast<uint4*>(vb + off) = vn;
+        if (hc == 0) {
+          *reinterpret_cast<uint4*>(x.k_cache + crow + lane * 8) = kn;
+          *reinterpret_cast<uint4*>(x.v_cache + crow + lane * 8) = vn;
+        }
+      }
+    }
+    if (n_valid < OT) {
+      // rows past the length may hold anything: zero V there, so that a weight
+      // of zero adds zero
+      for (int idx = lane; idx < (OT - n_valid) * CB * 8; idx += 32) {
+        const int rr = n_valid + idx / (CB * 8), rem = idx % (CB * 8);
+        *reinterpret_cast<uint4*>(vb + (rem / 8) * BLOCK_BYTES + sw128_offset(rr, rem % 8)) =
+            make_uint4(0, 0, 0, 0);
+      }
+    }
+    if (patch || n_valid < OT) {
+      fence_proxy_async_smem();  // (a copy lands here next)
+      __syncwarp();
+    }
+    // ---- S^T = K Q^T, in two chains
+    float sc[2][4] = {};
+    const uint32_t kbase = smem_u32(kb), vbase = smem_u32(vb);
+    const int krow = (mat & 1) * 8 + r8;
+#pragma unroll
+    for (int kk = 0; kk < KSTEPS; ++kk) {
+      const int col = kk * 16 + (mat >> 1) * 8;
+      uint32_t a0, a1, a2, a3;
+      ldsm_x4(kbase + (col / 64) * BLOCK_BYTES + sw128_offset(krow, (col % 64) / 8), a0, a1, a2, a3);
+      mma_bf16_16816(sc[kk & 1], a0, a1, a2, a3, qf[kk][0], qf[kk][1]);
+    }
+    // (key g, head 2t) (key g, head 2t + 1) (key g + 8, 2t) (key g + 8, 2t + 1)
+    float pr[4], alpha[2];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      pr[e] = g + (e >> 1) * 8 < n_valid ? (sc[0][e] + sc[1][e]) * x.scale_log2 : -INFINITY;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float mx = fmaxf(pr[h], pr[h + 2]);
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      const float m_new = fmaxf(m_run[h], mx);
+      const float ref = m_new == -INFINITY ? 0.f : m_new;
+      alpha[h] = m_run[h] == -INFINITY ? 0.f : ex2_approx(m_run[h] - ref);
+      pr[h] = ex2_approx(pr[h] - ref);
+      pr[h + 2] = ex2_approx(pr[h + 2] - ref);
+      l_run[h] = fmaf(l_run[h], alpha[h], pr[h] + pr[h + 2]);
+      m_run[h] = m_new;
+    }
+#pragma unroll
+    for (int mt = 0; mt < KSTEPS; ++mt) {
+      o[mt][0] *= alpha[0];
+      o[mt][1] *= alpha[1];
+      o[mt][2] *= alpha[0];
+      o[mt][3] *= alpha[1];
+    }
+    // P rounded to bf16 for the product; the sum is of the unrounded values
+    const uint32_t pb0 = movmatrix_t(pack_bf16x2(pr[0], pr[1]));
+    const uint32_t pb1 = movmatrix_t(pack_bf16x2(pr[2], pr[3]));
+    // ---- O^T += V^T P^T
+    const int vrow = (mat >> 1) * 8 + r8;
+#pragma unroll
+    for (int mt = 0; mt < KSTEPS; ++mt) {
+      const int col = mt * 16 + (mat & 1) * 8;
+      uint32_t a0, a1, a2, a3;
+      ldsm_x4_t(vbase + (col / 64) * BLOCK_BYTES + sw128_offset(vrow, (col % 64) / 8), a0, a1, a2,
+                a3);
+      mma_bf16_16816(o[mt], a0, a1, a2, a3, pb0, pb1);
+    }
+    __syncwarp();
+    if (i + OS < x1) fetch(i + OS);
+    if (i + 1 == x1 || at.c + 1 == at.n) {  // the segment ends: its partial
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 4);
+        l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 8);
+        l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 16);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int hh = 2 * t + h;
+        if (hc * 8 + hh < x.group) {
+          float* dst = home
+              ? x.own_home + (static_cast<size_t>(at.b) * x.H + kvh * x.group + hc * 8 + hh) *
+                                 dec::part_stride(D)
+              : x.own_mid + (static_cast<size_t>(worker) * 8 + hh) * dec::part_stride(D);
+#pragma unroll
+          for (int mt = 0; mt < KSTEPS; ++mt) {
+            dst[mt * 16 + g] = o[mt][h];
+            dst[mt * 16 + g + 8] = o[mt][h + 2];
+          }
+          if (g == 0) {
+            dst[D] = m_run[h];
+            dst[D + 1] = l_run[h];
+          }
+        }
+      }
+    }
+    advance(at);
+  }
+}
+
 template <int D>
 constexpr size_t prefix_smem_bytes() {
-  return (sizeof(PrefixSmem<D>) > sizeof(DecSmem<D>) ? sizeof(PrefixSmem<D>) : sizeof(DecSmem<D>)) +
+  return (sizeof(PrefixSmem<D>) > sizeof(OwnSmem<D>) ? sizeof(PrefixSmem<D>) : sizeof(OwnSmem<D>)) +
          1024;
 }
 
@@ -576,160 +878,170 @@ __global__ void __launch_bounds__(px::THREADS, 1)
     decode_prefix_kernel(const __grid_constant__ CUtensorMap tm_kp,
                          const __grid_constant__ CUtensorMap tm_vp,
                          const __grid_constant__ CUtensorMap tm_k,
-                         const __grid_constant__ CUtensorMap tm_v, PrefixParams x, DecodeParams p) {
+                         const __grid_constant__ CUtensorMap tm_v,
+                         const __grid_constant__ PrefixParams x) {
+  using namespace px;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  DecSmem<D>& own = *reinterpret_cast<DecSmem<D>*>(smem);
+  OwnSmem<D>& own = *reinterpret_cast<OwnSmem<D>*>(smem);
   // a programmatic dependent of what precedes it: no global memory before this
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  scan_chunks<APPEND, px::THREADS>(own.chunk_prefix, p);
-  const long long n_chunks = static_cast<long long>(own.chunk_prefix[p.bsz]) * p.Hkv * p.hchunks;
-  const PrefixPlan plan = prefix_plan(x, n_chunks, gridDim.x, px::cost_pair(D), px::cost_single(D),
-                                      px::cost_chunk(D));
-  if (blockIdx.x == 0) {  // for the combine kernel
-    if (threadIdx.x == 0) {
-      x.hdr[0] = plan.groups;
-      x.hdr[1] = plan.per;
-      x.hdr[2] = plan.own;
-    }
-    for (int b = threadIdx.x; b <= p.bsz; b += px::THREADS) p.ws_prefix[b] = own.chunk_prefix[b];
-  }
+  scan_tiles<APPEND>(own.before, x);
+  const int n_tiles = own.before[x.b] * x.Hkv * x.hchunks;
+  const PrefixPlan plan =
+      prefix_plan(x, n_tiles, gridDim.x, cost_pair(D), cost_single(D), cost_tile(D));
+  const int n_workers = min(n_tiles, plan.own * OW);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int cta = blockIdx.x, n_prefix = plan.groups * plan.per;
   if (cta < n_prefix) {
-    const long long items = static_cast<long long>(x.Hkv) * x.nt * (x.pairs / plan.groups);
-    const int group = cta / plan.per, i = cta - group * plan.per;
-    __syncthreads();  // the scan's shared memory is free: CTA 0 has read it
-    prefix_share<D>(*reinterpret_cast<PrefixSmem<D>*>(smem), tm_kp, tm_vp, x, cta,
-                    group * items + share_start(i, items, plan.per),
-                    group * items + share_start(i + 1, items, plan.per));
+    // the scan's shared memory has been read, and the ring's copies may land there
+    fence_proxy_async_smem();
+    __syncthreads();
+    prefix_share<D>(*reinterpret_cast<PrefixSmem<D>*>(smem), tm_kp, tm_vp, x, plan, cta);
     return;
   }
-  if (cta - n_prefix >= plan.own) return;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < dec::NSTAGE; ++i) {
-      mbar_init(&own.full[i], 1);
-      mbar_init(&own.empty[i], dec::NCW);
-    }
+  // warps of one CTA are workers plan.own apart, so that few tiles spread over the SMs
+  const int worker = cta - n_prefix + (threadIdx.x >> 5) * plan.own;
+  if (cta - n_prefix >= plan.own || worker >= n_workers) return;
+  if ((threadIdx.x & 31) == 0) {
+    for (int i = 0; i < OS; ++i) mbar_init(&own.full[threadIdx.x >> 5][i], 1);
     fence_mbar_init();
   }
-  __syncthreads();
-  if (threadIdx.x >= dec::THREADS) return;
-  decode_share<D, APPEND>(own, tm_k, tm_v, p, cta - n_prefix, plan.own);
+  __syncwarp();
+  own_share<D, APPEND>(own, tm_k, tm_v, x, worker, n_workers, n_tiles);
 }
 
-// Merges the partials of 32 query rows of one K/V head, 8 dimensions a block:
-// a lane is a row, and the eight warps take the partials in turn (a short batch
-// behind a long prefix has over a hundred of them) and are merged through
-// shared memory.
+// Merges the partials of 32 query rows of one K/V head: a lane is a row, a warp
+// 8 of its dimensions, and WK warps with the same dimensions take the partials
+// in turn and are merged through shared memory.  Four partials are loaded at a
+// time.
 namespace px {
 constexpr int COMBINE_WARPS = 8;
 }
-template <int D>
-__global__ void __launch_bounds__(px::COMBINE_WARPS * 32)
-    decode_prefix_combine_kernel(PrefixParams x, DecodeParams p, __nv_bfloat16* __restrict__ out) {
+template <int D, int WK>
+__global__ void __launch_bounds__(px::COMBINE_WARPS * 32, 3)
+    decode_prefix_combine_kernel(const __grid_constant__ PrefixParams x, int append,
+                                 __nv_bfloat16* __restrict__ out) {
   using namespace px;
-  constexpr int DC = D / 8;
-  constexpr int W = COMBINE_WARPS;
-  __shared__ float so[W][8][33], sm[W][33], sl[W][33];
+  constexpr int WD = COMBINE_WARPS / WK;  // warps side by side over the dimensions
+  constexpr int DC = D / (8 * WD);        // blocks over the dimensions
+  constexpr int U = 4;
+  __shared__ float so[COMBINE_WARPS][10][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int d0 = static_cast<int>(blockIdx.x % DC) * 8;
+  const int wk = warp / WD, wd = warp - wk * WD;
   const int rb = static_cast<int>(blockIdx.x / DC);
+  const int d0 = (static_cast<int>(blockIdx.x - rb * DC) * WD + wd) * 8;
   const int blocks_per_kvh = (x.rows + 31) / 32;
   const int kvh = rb / blocks_per_kvh;
   const int row0 = (rb - kvh * blocks_per_kvh) * 32;
-  const int row = row0 + lane;
-  const bool valid = row < x.rows;
+  const bool valid = row0 + lane < x.rows;
+  const int row = min(row0 + lane, x.rows - 1);
+  const int b = row / x.group, h = row - b * x.group;
+  const int pair = row0 / (2 * BM), in_pair = row0 - pair * 2 * BM;
+  const bool single = x.rows - pair * 2 * BM <= BM;
+  const int seq = pair * x.Hkv + kvh;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int groups = x.hdr[0], per = x.hdr[1], n_own = x.hdr[2];
+  const int2 pre = x.nt > 0 ? x.part_of[seq] : make_int2(0, 0);
+  int2 own = x.own_of[(b * x.Hkv + kvh) * x.hchunks + h / 8];
+  if (attend_len(x.lens[b], x.L, append) == 0) own = make_int2(0, 0);  // (nothing was noted)
+
   float m = -INFINITY, l = 0.f, o[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) o[e] = 0.f;
-  auto add = [&](float mc, float lc, const float (&oc)[8]) {
-    if (lc == 0.f) return;  // (no weight in it; a NaN sum is not 0 and stays)
-    const float m_new = fmax3_nan(m, mc, mc);
-    const float fo = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
-    const float fc = ex2_approx(mc - m_new);
-    l = l * fo + lc * fc;
+  // merges U partials; one that is not there has the maximum -inf and zeros
+  auto add = [&](const float (&mc)[U], const float (&lc)[U], const float (&oc)[U][8]) {
+    float top = m;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = o[e] * fo + oc[e] * fc;
-    m = m_new;
+    for (int u = 0; u < U; ++u) top = fmax3_nan(top, mc[u], mc[u]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float f = ex2_approx(m - ref);
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] *= f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float w = ex2_approx(mc[u] - ref);
+      l = fmaf(w, lc[u], l);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = fmaf(w, oc[u][e], o[e]);
+    }
+    m = top;
   };
-
-  // ---- prefix partials: the home slot, then those of the CTAs whose run starts
-  // inside this (tile pair, K/V head); two units each if they share their rows
-  int taken = 0;  // partials dealt out to the warps so far
-  if (groups > 0) {
-    const int pair = row0 / (2 * BM), in_pair = row0 - pair * 2 * BM;
-    const bool single = x.rows - pair * 2 * BM <= BM;
-    const int seq = pair * x.Hkv + kvh;
-    const long long first = static_cast<long long>(seq) * x.nt;
-    const long long items = static_cast<long long>(x.Hkv) * x.nt * (x.pairs / groups);
-    const long long group = first / items, at = first - group * items;
-    const int c0 = static_cast<int>(group * per + share_owner(at, items, per));
-    const int c1 = static_cast<int>(group * per + share_owner(at + x.nt - 1, items, per));
-    const int n = (c1 - c0 + 1) << single;
-    for (int k = warp; k < n; k += W) {
-      const int seg = k >> single;
-      const int unit = single ? k & 1 : in_pair / BM;
-      const int slot = seg == 0 ? seq : x.pairs * x.Hkv + c0 + seg;
-      const float* src = x.part + (static_cast<size_t>(slot) * 2 + unit) * unit_floats(D) +
-                         in_pair % BM + lane;
-      if (valid) {
-        float oc[8];
-        const float mc = src[D * BM], lc = src[(D + 1) * BM];
+  // ---- prefix: the home slot, then those of the CTAs that follow its CTA; two
+  // units each if they share their rows
+  const int n_pre = pre.y << single;
+  const float* base = x.part + in_pair / BM * unit_floats(D) + in_pair % BM + lane;
+  for (int k0 = wk; k0 < n_pre; k0 += U * WK) {
+    float mc[U], lc[U], oc[U][8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) oc[e] = src[(d0 + e) * BM];
-        add(mc, lc, oc);
-      }
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * WK;
+      const int seg = k >> single;
+      const int slot = seg == 0 ? seq : x.pairs * x.Hkv + pre.x + seg;
+      const float* src = base + static_cast<long long>(2 * slot + (single ? k & 1 : 0)) * unit_floats(D);
+      const bool there = valid && k < n_pre;
+      mc[u] = there ? src[D * BM] : -INFINITY;
+      lc[u] = there ? src[(D + 1) * BM] : 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) oc[u][e] = there ? src[(d0 + e) * BM] : 0.f;
     }
-    taken = n;
+    add(mc, lc, oc);
   }
-  // ---- the sequence's own partials, laid out as decode_share writes them
-  if (valid) {
-    const int b = row / x.group, h = row - b * x.group;
-    const int hc = h / 8;
-    const long long before = p.ws_prefix[b];
-    const int nch = static_cast<int>(p.ws_prefix[b + 1] - before);
-    if (nch > 0) {
-      const int per_b = p.Hkv * p.hchunks;
-      const long long n_chunks = static_cast<long long>(p.ws_prefix[p.bsz]) * per_b;
-      const long long at = before * per_b + static_cast<long long>(kvh * p.hchunks + hc) * nch;
-      const int c0 = static_cast<int>(share_owner(at, n_chunks, n_own));
-      const int c1 = static_cast<int>(share_owner(at + nch - 1, n_chunks, n_own));
-      for (int k = (warp + W - taken % W) % W; k <= c1 - c0; k += W) {
-        const float* src = k == 0
-            ? p.ws_home + (static_cast<size_t>(b) * p.H + kvh * x.group + h) * dec::part_stride(D)
-            : p.ws_cta + (static_cast<size_t>(c0 + k) * 8 + h % 8) * dec::part_stride(D);
-        const float4 a = *reinterpret_cast<const float4*>(src + d0);
-        const float4 c = *reinterpret_cast<const float4*>(src + d0 + 4);
-        const float oc[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-        add(src[D], src[D + 1], oc);
-      }
+  // ---- own rows: the home slot, then those of the workers that follow
+  for (int k0 = (wk + WK - n_pre % WK) % WK; k0 < own.y; k0 += U * WK) {
+    float mc[U], lc[U], oc[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * WK;
+      const float* src = k == 0
+          ? x.own_home + (static_cast<size_t>(b) * x.H + kvh * x.group + h) * dec::part_stride(D)
+          : x.own_mid + (static_cast<size_t>(own.x + k) * 8 + h % 8) * dec::part_stride(D);
+      const bool there = k < own.y;
+      const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 a = there ? *reinterpret_cast<const float4*>(src + d0) : z;
+      const float4 c = there ? *reinterpret_cast<const float4*>(src + d0 + 4) : z;
+      const float2 ml = there ? *reinterpret_cast<const float2*>(src + D) : make_float2(-INFINITY, 0.f);
+      mc[u] = ml.x, lc[u] = ml.y;
+      oc[u][0] = a.x, oc[u][1] = a.y, oc[u][2] = a.z, oc[u][3] = a.w;
+      oc[u][4] = c.x, oc[u][5] = c.y, oc[u][6] = c.z, oc[u][7] = c.w;
     }
+    add(mc, lc, oc);
   }
-  sm[warp][lane] = m;
-  sl[warp][lane] = l;
+  so[warp][8][lane] = m;
+  so[warp][9][lane] = l;
 #pragma unroll
   for (int e = 0; e < 8; ++e) so[warp][e][lane] = o[e];
   __syncthreads();
-  const int orow = threadIdx.x >> 3, e = threadIdx.x & 7;
-  if (row0 + orow < x.rows) {
-    float top = -INFINITY, sum = 0.f, acc = 0.f;
+  // a warp takes 8 / WK of its dimensions over all WK warps that have them
+  constexpr int E = 8 / WK;
+  const int e0 = wk * E;
+  float top = -INFINITY, sum = 0.f, acc[E];
 #pragma unroll
-    for (int w = 0; w < W; ++w) top = fmax3_nan(top, sm[w][orow], sm[w][orow]);
+  for (int w = 0; w < WK; ++w) {
+    const float mw = so[w * WD + wd][8][lane];
+    top = fmax3_nan(top, mw, mw);
+  }
+  const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const float mw = sm[w][orow];
-      const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - top);
-      sum = fmaf(f, sl[w][orow], sum);
-      acc = fmaf(f, so[w][e][orow], acc);
-    }
-    const int r = row0 + orow, b = r / x.group, h = r - b * x.group;
-    out[(static_cast<size_t>(b) * x.H + kvh * x.group + h) * D + d0 + e] =
-        __float2bfloat16_rn(sum == 0.f ? 0.f : acc / sum);
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+  for (int w = 0; w < WK; ++w) {
+    const float f = ex2_approx(so[w * WD + wd][8][lane] - ref);
+    sum = fmaf(f, so[w * WD + wd][9][lane], sum);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(f, so[w * WD + wd][e0 + e][lane], acc[e]);
+  }
+  if (!valid) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  __nv_bfloat16* dst = out + (static_cast<size_t>(b) * x.H + kvh * x.group + h) * D + d0 + e0;
+  if constexpr (E == 1) {
+    *dst = __float2bfloat16_rn(acc[0] * inv);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
   }
 }
 

@@ -426,7 +426,7 @@ int launch_dependent(void (*kernel)(P...), long long blocks, int threads, size_t
 // Layout of the workspace.
 struct PrefixLayout {
   int nt, pairs;
-  size_t home, ctas, hdr, bytes;  // offsets of the own rows' partials, the ints, and the end
+  size_t home, mid, part_of, own_of, bytes;  // offsets of PrefixParams' arrays, and the end
 };
 PrefixLayout prefix_layout(int bsz, int H, int Hkv, int P, int D) {
   using namespace la::px;
@@ -439,9 +439,10 @@ PrefixLayout prefix_layout(int bsz, int H, int Hkv, int P, int D) {
   const size_t slots = w.nt == 0 ? 0 : seqs + std::min<size_t>(seqs * w.nt, MAX_CTAS);
   w.home = up(slots * 2 * unit_floats(D) * sizeof(float));
   const size_t row = la::dec::part_stride(D) * sizeof(float);
-  w.ctas = w.home + up(static_cast<size_t>(bsz) * H * row);
-  w.hdr = w.ctas + up(static_cast<size_t>(MAX_CTAS) * 8 * row);
-  w.bytes = w.hdr + up((HDR + static_cast<size_t>(bsz) + 1) * sizeof(int));
+  w.mid = w.home + up(static_cast<size_t>(bsz) * H * row);
+  w.part_of = w.mid + up(static_cast<size_t>(MAX_CTAS) * OW * 8 * row);
+  w.own_of = w.part_of + up(seqs * sizeof(int2));
+  w.bytes = w.own_of + up(static_cast<size_t>(bsz) * Hkv * ((H / Hkv + 7) / 8) * sizeof(int2));
   return w;
 }
 
@@ -457,6 +458,11 @@ int decode_prefix(const void* q, const void* k_new, const void* v_new, const voi
                   void* k_cache, void* v_cache, const int* lens, int bsz, int H, int Hkv, int L,
                   float scale, void* out, void* workspace, cudaStream_t st) {
   const PrefixLayout w = prefix_layout(bsz, H, Hkv, P, D);
+  // items and tiles are counted in 32 bits
+  const long long seqs = static_cast<long long>(bsz) * Hkv * ((H / Hkv + 7) / 8);
+  if (static_cast<long long>(w.pairs) * Hkv * w.nt > 0x7fffffffLL ||
+      seqs * (L / la::px::OT + 1) > 0x7fffffffLL)
+    return LLAMA_ERR_UNSUPPORTED;
   CUtensorMap tkp{}, tvp{}, tk, tv;
   if (P > 0) {
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(P),
@@ -470,7 +476,7 @@ int decode_prefix(const void* q, const void* k_new, const void* v_new, const voi
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(L),
                               static_cast<cuuint64_t>(bsz) * Hkv};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(L) * D * 2};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(la::dec::TR), 1};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(la::px::OT), 1};
   if (!make_map(&tk, k_cache, 3, dims, strides, box)) return LLAMA_ERR_CUDA;
   if (!make_map(&tv, v_cache, 3, dims, strides, box)) return LLAMA_ERR_CUDA;
   const int n_ctas = std::min(sm_count(), la::px::MAX_CTAS);
@@ -479,47 +485,53 @@ int decode_prefix(const void* q, const void* k_new, const void* v_new, const voi
   la::PrefixParams x;
   x.q = static_cast<const __nv_bfloat16*>(q);
   x.part = reinterpret_cast<float*>(ws);
-  x.hdr = reinterpret_cast<int*>(ws + w.hdr);
+  x.own_home = reinterpret_cast<float*>(ws + w.home);
+  x.own_mid = reinterpret_cast<float*>(ws + w.mid);
+  x.part_of = reinterpret_cast<int2*>(ws + w.part_of);
+  x.own_of = reinterpret_cast<int2*>(ws + w.own_of);
   x.rows = bsz * (H / Hkv);
   x.P = P;
   x.nt = w.nt;
   x.pairs = w.pairs;
+  x.b = bsz;
   x.H = H;
   x.Hkv = Hkv;
+  x.L = L;
   x.group = H / Hkv;
+  x.hchunks = (x.group + 7) / 8;
+  x.lens = lens;
+  x.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  x.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  x.k_cache = static_cast<__nv_bfloat16*>(k_cache);
+  x.v_cache = static_cast<__nv_bfloat16*>(v_cache);
   x.scale_log2 = scale * 1.4426950408889634f;
-  la::DecodeParams p{};
-  p.q = x.q;
-  p.lens = lens;
-  p.k_new = static_cast<const __nv_bfloat16*>(k_new);
-  p.v_new = static_cast<const __nv_bfloat16*>(v_new);
-  p.k_cache = static_cast<__nv_bfloat16*>(k_cache);
-  p.v_cache = static_cast<__nv_bfloat16*>(v_cache);
-  p.ws_home = reinterpret_cast<float*>(ws + w.home);
-  p.ws_cta = reinterpret_cast<float*>(ws + w.ctas);
-  p.ws_prefix = x.hdr + la::px::HDR;
-  p.bsz = bsz;
-  p.H = H;
-  p.Hkv = Hkv;
-  p.L = L;
-  p.group = x.group;
-  p.hchunks = (p.group + 7) / 8;
-  p.scale_log2 = x.scale_log2;
   constexpr size_t smem = la::prefix_smem_bytes<D>();
+  const int append = k_new != nullptr;
   int e;
-  if (k_new != nullptr) {
+  if (append) {
     if (!ensure_smem_attr<la::decode_prefix_kernel<D, true>>(smem)) return LLAMA_ERR_CUDA;
     e = launch_dependent(la::decode_prefix_kernel<D, true>, n_ctas, la::px::THREADS, smem, st,
-                         "prefix decode", tkp, tvp, tk, tv, x, p);
+                         "prefix decode", tkp, tvp, tk, tv, x);
   } else {
     if (!ensure_smem_attr<la::decode_prefix_kernel<D, false>>(smem)) return LLAMA_ERR_CUDA;
     e = launch_dependent(la::decode_prefix_kernel<D, false>, n_ctas, la::px::THREADS, smem, st,
-                         "prefix decode", tkp, tvp, tk, tv, x, p);
+                         "prefix decode", tkp, tvp, tk, tv, x);
   }
   if (e) return e;
-  const long long blocks = (static_cast<long long>(x.rows) + 31) / 32 * Hkv * (D / 8);
-  return launch_dependent(la::decode_prefix_combine_kernel<D>, blocks, la::px::COMBINE_WARPS * 32, 0,
-                          st, "prefix combine", x, p, static_cast<__nv_bfloat16*>(out));
+  // the combine kernel's blocks in one wave (three to an SM): the fewer rows there
+  // are, the more warps share the partials of one
+  const long long row_blocks = (static_cast<long long>(x.rows) + 31) / 32 * Hkv;
+  auto combine = [&](auto wk) {
+    constexpr int WK = decltype(wk)::value;
+    return launch_dependent(la::decode_prefix_combine_kernel<D, WK>, row_blocks * (D / 64) * WK,
+                            la::px::COMBINE_WARPS * 32, 0, st, "prefix combine", x, append,
+                            static_cast<__nv_bfloat16*>(out));
+  };
+  const long long fit = 3LL * n_ctas / (row_blocks * (D / 64));
+  if (fit >= 8) return combine(std::integral_constant<int, 8>{});
+  if (fit >= 4) return combine(std::integral_constant<int, 4>{});
+  if (fit >= 2) return combine(std::integral_constant<int, 2>{});
+  return combine(std::integral_constant<int, 1>{});
 }
 
 // ---------------------------------------------------------------- scaled tables and rotation
