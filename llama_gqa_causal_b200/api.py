@@ -15,6 +15,7 @@ is not supported (include/llama_attn.h states the same for the C ABI).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional, Tuple
@@ -171,7 +172,7 @@ def _need(t: Optional[torch.Tensor], where: str, name: str, dtype: torch.dtype,
         raise ValueError(f"{where}: {name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{where}: {name} is on {t.device}, expected {device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{where}: {name} must hold {numel} elements, got {t.numel()}")
@@ -229,24 +230,31 @@ def rope_table_ntk(pos: torch.Tensor, head_dim: int, theta: float = 10000.0, alp
 
 def _on(device: torch.device, where: str, fn, args, stream):
     """Call a library function on the tensors' own device: a launch goes to the
-    current device, which need not be theirs."""
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)), where)
-        return
-    with torch.cuda.device(device):
-        _check(fn(*args, _stream(stream)), where)
+    current device, which need not be theirs.  (The raw-stream and current-device
+    calls are what torch.cuda's own wrappers end in; the wrappers take longer than
+    a decode step's kernel.)"""
+    index = device.index
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, s)
+    if status != LLAMA_OK:
+        raise LlamaAttnError(status, where)
 
 
 def _table_scaled(where: str, pos: torch.Tensor, head_dim: int, args, stream):
     fn = getattr(load(), where)
-    pos = pos.to(torch.int64).contiguous()
+    if pos.dtype is not torch.int64 or not pos.is_contiguous():
+        pos = pos.to(torch.int64).contiguous()
     p = _ptr(pos)
-    cos = torch.empty(*pos.shape, head_dim, device=pos.device, dtype=torch.float32)
+    shape, dev = pos.shape, pos.device
+    cos = torch.empty((*shape, head_dim), device=dev, dtype=torch.float32)
     sin = torch.empty_like(cos)
-    n = pos.numel()
-    bsz = pos.shape[0] if pos.dim() > 1 else 1
-    _on(pos.device, where, fn, (p, bsz, n // max(bsz, 1), head_dim, *args, cos.data_ptr(),
-                                sin.data_ptr()), stream)
+    bsz = shape[0] if len(shape) > 1 else 1
+    _on(dev, where, fn, (p, bsz, pos.numel() // max(bsz, 1), head_dim, *args, cos.data_ptr(),
+                         sin.data_ptr()), stream)
     return cos, sin
 
 
@@ -276,15 +284,14 @@ _Strides = ctypes.c_longlong * 3
 _PrefixStrides = ctypes.c_longlong * 2
 
 
-def _rope_view(t: torch.Tensor, where: str, name: str, dtype, device, tokens):
+def _rope_view(t: torch.Tensor, where: str, name: str, dtype, device, shape):
     """(pointer, strides of batch entry, token and head) of [b, s, heads, D] or [s, heads, D]."""
     if not t.is_cuda:
         raise ValueError("llama_attn: tensors must live on a CUDA device")
     if t.dtype != dtype or t.device != device:
         raise ValueError(f"{where}: {name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
-    if t.shape[:-2] != tokens or t.dim() != len(tokens) + 2:
-        raise ValueError(f"{where}: {name} must be [{', '.join(map(str, tokens))}, heads, head_dim], "
-                         f"got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{where}: {name} must be {list(shape)}, got {list(t.shape)}")
     st = t.stride()
     if st[-1] != 1:
         raise ValueError(f"{where}: the dimensions of a head of {name} must be adjacent")
@@ -300,35 +307,36 @@ def rope_apply(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, si
     in place; k's: rows of a cache).  transpose: the gradient of the rotation."""
     w = "llama_rope_apply"
     fn = load().llama_rope_apply
-    if q.dim() not in (3, 4):
+    shape, dev, dt = q.shape, q.device, q.dtype
+    if len(shape) == 4:
+        b, s, H, D = shape
+    elif len(shape) == 3:
+        b, (s, H, D) = 1, shape
+    else:
         raise ValueError(f"{w}: q must be [b, s, heads, head_dim] or [s, heads, head_dim]")
-    tokens, H, D = q.shape[:-2], q.shape[-2], q.shape[-1]
-    b, s = tokens if len(tokens) == 2 else (1, tokens[0])
     R = cos.shape[-1]
-    dev, dt = q.device, q.dtype
     _tables(cos, sin, w, dev, b * s, R)
     if sin.shape != cos.shape:
         raise ValueError(f"{w}: cos and sin must have one shape")
-    qp, qs = _rope_view(q, w, "q", dt, dev, tokens)
+    qp, qs = _rope_view(q, w, "q", dt, dev, shape)
     q_out, k_out = out if out is not None else (None, None)
     if q_out is None:
-        q_out = torch.empty(q.shape, device=dev, dtype=dt)
-    elif q_out.shape != q.shape:
-        raise ValueError(f"{w}: out must have the shapes of q and k")
-    qop, qos = _rope_view(q_out, w, "out", dt, dev, tokens)
-    Hkv = kp = ks = kop = kos = None
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    qop, qos = _rope_view(q_out, w, "out", dt, dev, shape)
+    Hkv, kp, ks, kop, kos = 0, None, None, None, None
     if k is not None:
-        kp, ks = _rope_view(k, w, "k", dt, dev, tokens)
-        Hkv = k.shape[-2]
+        k_shape = k.shape
+        if k_shape[:-2] != shape[:-2] or k_shape[-1] != D:
+            raise ValueError(f"{w}: k must have q's tokens and head_dim")
+        Hkv = k_shape[-2]
+        kp, ks = _rope_view(k, w, "k", dt, dev, k_shape)
         if k_out is None:
-            k_out = torch.empty(k.shape, device=dev, dtype=dt)
-        if k.shape[-1] != D or k_out.shape != k.shape:
-            raise ValueError(f"{w}: k must have q's head_dim, and out the shapes of q and k")
-        kop, kos = _rope_view(k_out, w, "out", dt, dev, tokens)
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        kop, kos = _rope_view(k_out, w, "out", dt, dev, k_shape)
     elif k_out is not None:
         raise ValueError(f"{w}: an output for k needs k")
-    _on(dev, w, fn, (qp, kp, _ptr(cos), _ptr(sin), b, s, H, Hkv or 0, D, R, int(bool(interleaved)),
-                     int(bool(transpose)), qs, ks, qop, kop, qos, kos, _dtype_code(dt)), stream)
+    _on(dev, w, fn, (qp, kp, _ptr(cos), _ptr(sin), b, s, H, Hkv, D, R, 1 if interleaved else 0,
+                     1 if transpose else 0, qs, ks, qop, kop, qos, kos, _dtype_code(dt)), stream)
     return q_out, k_out
 
 
@@ -601,6 +609,7 @@ def decode_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def decode_prefix_workspace_bytes(bsz, n_heads, n_kv_heads, prefix_len, head_dim) -> int:
     return int(load().llama_attn_decode_prefix_workspace_bytes(bsz, n_heads, n_kv_heads, prefix_len,
                                                                head_dim))
@@ -611,13 +620,13 @@ def _prefix_view(t: torch.Tensor, name: str, like: torch.Tensor, Hkv: int, P: in
     w = "llama_attn_decode_prefix"
     if not t.is_cuda:
         raise ValueError("llama_attn: tensors must live on a CUDA device")
-    _need(t, w, name, like.dtype, like.device, shape=(Hkv, P, D))
-    st = t.stride()
-    if st[2] != 1:
+    _need(t, w, name, like.dtype, like.device, (Hkv, P, D))
+    head, row, one = t.stride()
+    if one != 1:
         raise ValueError(f"{w}: the dimensions of a row of {name} must be adjacent")
     # the stride of an extent of one is never used; torch leaves it arbitrary
-    row = st[1] if P > 1 else D
-    return t.data_ptr(), _PrefixStrides(st[0] if Hkv > 1 else P * row, row)
+    row = row if P > 1 else D
+    return t.data_ptr(), _PrefixStrides(head if Hkv > 1 else P * row, row)
 
 
 def decode_prefix(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor,
@@ -635,25 +644,33 @@ def decode_prefix(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tenso
     Hkv, L = k_cache.shape[1], k_cache.shape[2]
     P = k_prefix.shape[1]
     dev = q.device
-    _need(k_cache, w, "k_cache", q.dtype, dev, shape=(b, Hkv, L, D))
-    _need(v_cache, w, "v_cache", q.dtype, dev, shape=(b, Hkv, L, D))
-    _need(cache_lens, w, "cache_lens", torch.int32, dev, numel=b)
-    _need(k_new, w, "k_new", q.dtype, dev, shape=(b, Hkv, D))
-    _need(v_new, w, "v_new", q.dtype, dev, shape=(b, Hkv, D))
-    _need(out, w, "out", q.dtype, dev, numel=b * H * D)
+    dt = q.dtype
+    _need(k_cache, w, "k_cache", dt, dev, (b, Hkv, L, D))
+    _need(v_cache, w, "v_cache", dt, dev, (b, Hkv, L, D))
+    _need(cache_lens, w, "cache_lens", torch.int32, dev, None, b)
+    kn = vn = None
+    if k_new is not None:
+        _need(k_new, w, "k_new", dt, dev, (b, Hkv, D))
+        kn = _ptr(k_new)
+    if v_new is not None:
+        _need(v_new, w, "v_new", dt, dev, (b, Hkv, D))
+        vn = _ptr(v_new)
+    _need(out, w, "out", dt, dev, None, b * H * D)
     kp, ks = _prefix_view(k_prefix, "k_prefix", q, Hkv, P, D)
     vp, vs = _prefix_view(v_prefix, "v_prefix", q, Hkv, P, D)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty(b, H * D, device=dev, dtype=q.dtype)
-    if workspace is None:
-        workspace = torch.empty(decode_prefix_workspace_bytes(b, H, Hkv, P, D), device=dev,
-                                dtype=torch.uint8)
-    ws_bytes = workspace.numel() * workspace.element_size()
-    _on(dev, w, fn, (_ptr(q), _ptr(k_new), _ptr(v_new), kp, vp, P, ks, vs, _ptr(k_cache),
-                     _ptr(v_cache), _ptr(cache_lens), b, H, Hkv, L, D, scale, _ptr(out),
-                     _ptr(workspace), ws_bytes, _dtype_code(q.dtype)), stream)
+        out = torch.empty((b, H * D), device=dev, dtype=dt)
+    if workspace is None:  # (this call's own: torch hands it over, nothing to check)
+        need = decode_prefix_workspace_bytes(b, H, Hkv, P, D)
+        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+        ws, ws_bytes = workspace.data_ptr(), need
+    else:
+        ws, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+    _on(dev, w, fn, (_ptr(q), kn, vn, kp, vp, P, ks, vs, _ptr(k_cache), _ptr(v_cache),
+                     _ptr(cache_lens), b, H, Hkv, L, D, scale, _ptr(out), ws, ws_bytes,
+                     _dtype_code(dt)), stream)
     return out
 
 

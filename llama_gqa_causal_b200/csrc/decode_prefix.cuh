@@ -48,7 +48,7 @@ static_assert(kRegsControl % 8 == 0 && kRegsSoftmax % 8 == 0, "setmaxnreg takes 
 static_assert(kRegsControl + 2 * kRegsSoftmax <= 3 * kRegsAtLaunch,
               "setmaxnreg split exceeds the registers the block is launched with");
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr int kPolyPairsOf8 = 3;  // pairs of 8 exponentiated on the FMA pipe
+constexpr int kPolyPairsOf8 = 1;  // pairs of 8 exponentiated on the FMA pipe
 // Work of an item and of a 16-row tile of a cache, in units that only their
 // ratios matter of: what one SM takes for it.
 __host__ __device__ constexpr float cost_pair(int d) { return d == 128 ? 2.1f : 1.5f; }
@@ -316,92 +316,85 @@ __device__ __forceinline__ void prefix_share(PrefixSmem<D>& s, const CUtensorMap
     auto issue_qk = [&](int t, int tq, int st) {  // S_t = Q_tq K^T
       const uint64_t qd = q_desc0 + ((static_cast<uint32_t>(tq) * TILE_BYTES) >> 4);
       const uint64_t kd = k_desc0 + ((static_cast<uint32_t>(st) * TILE_BYTES) >> 4);
-      if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk / 4) * BLOCK_BYTES + (kk % 4) * 32) >> 4;
-          mma_ss(tm_s(t), qd + off, kd + off, IDESC_QK, kk > 0 ? 1u : 0u);
-        }
-        tc_commit(&s.s_full[t]);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk / 4) * BLOCK_BYTES + (kk % 4) * 32) >> 4;
+        mma_ss(tm_s(t), qd + off, kd + off, IDESC_QK, kk > 0 ? 1u : 0u);
       }
-      __syncwarp();
+      tc_commit(&s.s_full[t]);
     };
     auto issue_pv = [&](int t, int st, bool accumulate, int h) {  // keys [64h, 64h + 64)
       const uint64_t vd = v_desc0 + ((static_cast<uint32_t>(st) * TILE_BYTES) >> 4);
-      if (elect_one()) {
 #pragma unroll
-        for (int kk = h * (BN / 32); kk < (h + 1) * (BN / 32); ++kk)
-          mma_ts(tm_o(t), tm_s(t) + kk * 8, vd + ((kk * 2048) >> 4), IDESC_PV,
-                 (accumulate || kk > h * (BN / 32)) ? 1u : 0u);
-      }
-      __syncwarp();
+      for (int kk = h * (BN / 32); kk < (h + 1) * (BN / 32); ++kk)
+        mma_ts(tm_o(t), tm_s(t) + kk * 8, vd + ((kk * 2048) >> 4), IDESC_PV,
+               (accumulate || kk > h * (BN / 32)) ? 1u : 0u);
     };
-    auto commit = [&](uint64_t* bar) {
-      if (elect_one()) tc_commit(bar);
-      __syncwarp();
-    };
-    // the ring: the next tile to be taken, and the parity of its full barrier
-    int next_st = 0;
-    uint32_t next_ph = 0;
-    auto take = [&](int& st) {
-      st = next_st;
-      if (!mbar_wait(&s.full[st], next_ph)) return false;
-      tc_fence_after();
-      if (++next_st == NST) {
-        next_st = 0;
-        next_ph ^= 1;
-      }
-      return true;
-    };
-    uint32_t cnt0 = 0, cnt1 = 0;  // P tiles of each unit so far
-    uint32_t seg = 0;
-    bool ok = true;
-    for (int i = x0; i < x1 && ok; ++seg) {
-      const PrefixSegment g = prefix_segment(x, i, x1);
-      i += g.n;
-      ok = mbar_wait(&s.q_ready[0], seg & 1) && mbar_wait(&s.q_ready[1], seg & 1);
-      // step u of a segment is unit u & 1's, whether the units share the key
-      // tiles (two steps a tile) or take them in turn
-      const int steps = g.single ? g.n : 2 * g.n;
-      int vs = 0, ks = 0;
-#pragma unroll 1
-      for (int u = -2; u < steps && ok; ++u) {
-        const int t = u & 1;
-        if (u >= 0) {  // O_t += P_t V
-          if ((g.single || t == 0) && !take(vs)) {
-            ok = false;
-            break;
-          }
-          const uint32_t ph = (t ? cnt1 : cnt0) & 1;
-          if (t) ++cnt1;
-          else ++cnt0;
-#pragma unroll 1
-          for (int h = 0; h < 2 && ok; ++h) {
-            ok = mbar_wait(h ? &s.p_hi[t] : &s.p_lo[t], ph);
-            if (!ok) break;
+    // one lane does it all: it alone waits, so nothing lies between a barrier and
+    // the products but their issue
+    if (elect_one()) {
+      // the ring: the next tile to be taken, and the parity of its full barrier
+      int next_st = 0;
+      uint32_t next_ph = 0;
+      auto take = [&](int& st) {
+        st = next_st;
+        if (!mbar_wait(&s.full[st], next_ph)) return false;
+        tc_fence_after();
+        if (++next_st == NST) {
+          next_st = 0;
+          next_ph ^= 1;
+        }
+        return true;
+      };
+      uint32_t ph0 = 0, ph1 = 0;  // parity of each unit's next P tile
+      uint32_t seg = 0;
+      bool ok = true;
+      for (int i = x0; i < x1 && ok; ++seg) {
+        const PrefixSegment g = prefix_segment(x, i, x1);
+        i += g.n;
+        ok = mbar_wait(&s.q_ready[0], seg & 1) && mbar_wait(&s.q_ready[1], seg & 1);
+        // step u of a segment is unit u & 1's, whether the units share the key
+        // tiles (two steps a tile) or take them in turn; the code is laid out for
+        // either unit, since what lies between a unit's P and the products is on
+        // the path of every tile
+        const int steps = g.single ? g.n : 2 * g.n;
+        int vs = 0, ks = 0;
+        auto step = [&](auto unit, int u) {
+          constexpr int t = decltype(unit)::value;
+          if (u >= 0) {  // O_t += P_t V
+            if ((g.single || t == 0) && !take(vs)) return false;
+            uint32_t& ph = t ? ph1 : ph0;
+            if (!mbar_wait(&s.p_lo[t], ph)) return false;
             tc_fence_after();
-            issue_pv(t, vs, u > 1 || h > 0, h);
+            issue_pv(t, vs, u > 1, 0);
+            if (!mbar_wait(&s.p_hi[t], ph)) return false;
+            tc_fence_after();
+            issue_pv(t, vs, true, 1);
+            ph ^= 1;
+            if (g.single || t == 1) tc_commit(&s.empty[vs]);
           }
-          if (!ok) break;
-          if (g.single || t == 1) commit(&s.empty[vs]);
-        }
-        if (u + 2 < steps) {  // S_t = Q K^T of the unit's next tile
-          if ((g.single || t == 0) && !take(ks)) {
-            ok = false;
-            break;
+          if (u + 2 < steps) {  // S_t = Q K^T of the unit's next tile
+            if ((g.single || t == 0) && !take(ks)) return false;
+            issue_qk(t, g.single ? 0 : t, ks);
+            if (g.single || t == 1) tc_commit(&s.empty[ks]);
+          } else {
+            // (a unit without a tile waits for this all the same: running ahead, it
+            // would complete two phases of q_ready between two of this warp's waits)
+            tc_commit(&s.o_full[t]);
           }
-          issue_qk(t, g.single ? 0 : t, ks);
-          if (g.single || t == 1) commit(&s.empty[ks]);
-        } else {
-          // (a unit without a tile waits for this all the same: running ahead, it
-          // would complete two phases of q_ready between two of this warp's waits)
-          commit(&s.o_full[t]);
+          return true;
+        };
+#pragma unroll 1
+        for (int u = -2; u < steps && ok; u += 2) {
+          ok = step(std::integral_constant<int, 0>{}, u);
+          if (ok && u + 1 < steps) ok = step(std::integral_constant<int, 1>{}, u + 1);
         }
       }
+      // every MMA has completed before the CTA can exit
+      tc_commit(&s.mma_done);
+      mbar_wait(&s.mma_done, 0);
     }
-    // every MMA this warp issued has completed before the CTA can exit
-    commit(&s.mma_done);
-    mbar_wait(&s.mma_done, 0);
+    __syncwarp();
   } else if (warp < 4) {
     setmaxnreg_dec<kRegsControl>();
     // warp 2 notes where the combine kernel finds the segments of every (tile

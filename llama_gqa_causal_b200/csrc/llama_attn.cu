@@ -738,8 +738,9 @@ int llama_rope_table_banded(const long long* pos, int bsz, int seq, int head_dim
       !std::isfinite(high_freq_factor))
     return LLAMA_ERR_INVALID_ARG;
   la::ScaledFreqs freqs;
+  const double log_theta = std::log(theta);
   for (int i = 0; i < head_dim / 2; ++i) {
-    const double w = std::exp(-(2.0 * i / head_dim) * std::log(theta));
+    const double w = std::exp(-(2.0 * i / head_dim) * log_theta);
     const double turns = original_len * w / (2.0 * kPi);
     const double keep = std::min(
         1.0, std::max(0.0, (turns - low_freq_factor) / (high_freq_factor - low_freq_factor)));
@@ -762,8 +763,9 @@ int llama_rope_table_yarn(const long long* pos, int bsz, int seq, int head_dim, 
   const double lo = std::max(std::floor(dim_of(beta_fast)), 0.0);
   const double hi = std::min(std::ceil(dim_of(beta_slow)), static_cast<double>(head_dim - 1));
   la::ScaledFreqs freqs;
+  const double log_theta = std::log(theta);
   for (int i = 0; i < head_dim / 2; ++i) {
-    const double w = std::exp(-(2.0 * i / head_dim) * std::log(theta));
+    const double w = std::exp(-(2.0 * i / head_dim) * log_theta);
     const double ramp = std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 0.001)));
     freqs.inv[i] = w * (ramp / factor + (1.0 - ramp));
   }
