@@ -116,6 +116,12 @@ __device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams& x, int n_t
       r.groups = 1;
       r.per = min(na, items * x.pairs);
     }
+    // whole CTAs to every K/V head of a group where that idles (or, if there are
+    // own rows to be had, hands over) few: a CTA with one segment is done sooner
+    // than one that turns from one head to the next
+    const int heads = x.Hkv * (x.pairs / r.groups);
+    const int over = r.per % heads;
+    if (r.per > heads && over * 8 <= r.per) r.per -= over;
   }
   r.own = min(n_tiles, n_ctas - r.groups * r.per);
   return r;
@@ -886,8 +892,13 @@ __global__ void __launch_bounds__(px::THREADS, 1)
       prefix_plan(x, n_tiles, gridDim.x, cost_pair(D), cost_single(D), cost_tile(D));
   const int n_workers = min(n_tiles, plan.own * OW);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int cta = blockIdx.x, n_prefix = plan.groups * plan.per;
-  if (cta < n_prefix) {
+  // own CTAs evenly among the others, so that no part of the chip has only the
+  // ones or the others on its way to memory
+  const int n = gridDim.x;
+  const int own_before = blockIdx.x * plan.own / n;
+  if ((blockIdx.x + 1) * plan.own / n == own_before) {
+    const int cta = blockIdx.x - own_before;
+    if (cta >= plan.groups * plan.per) return;
     // the scan's shared memory has been read, and the ring's copies may land there
     fence_proxy_async_smem();
     __syncthreads();
@@ -895,8 +906,8 @@ __global__ void __launch_bounds__(px::THREADS, 1)
     return;
   }
   // warps of one CTA are workers plan.own apart, so that few tiles spread over the SMs
-  const int worker = cta - n_prefix + (threadIdx.x >> 5) * plan.own;
-  if (cta - n_prefix >= plan.own || worker >= n_workers) return;
+  const int worker = own_before + (threadIdx.x >> 5) * plan.own;
+  if (worker >= n_workers) return;
   if ((threadIdx.x & 31) == 0) {
     for (int i = 0; i < OS; ++i) mbar_init(&own.full[threadIdx.x >> 5][i], 1);
     fence_mbar_init();
