@@ -49,11 +49,11 @@ static_assert(kRegsControl + 2 * kRegsSoftmax <= 3 * kRegsAtLaunch,
               "setmaxnreg split exceeds the registers the block is launched with");
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int kPolyPairsOf8 = 1;  // pairs of 8 exponentiated on the FMA pipe
-// Work of an item and of a 16-row tile of a cache, in units that only their
+// Work of an item and of a step through the own rows (16 of them), in units that only their
 // ratios matter of: what one SM takes for it.
 __host__ __device__ constexpr float cost_pair(int d) { return d == 128 ? 2.1f : 1.5f; }
 __host__ __device__ constexpr float cost_single(int d) { return d == 128 ? 1.2f : 0.8f; }
-__host__ __device__ constexpr float cost_tile(int d) { return d == 128 ? 0.12f : 0.07f; }
+__host__ __device__ constexpr float cost_step(int d) { return d == 128 ? 0.12f : 0.07f; }
 __host__ __device__ constexpr float cost_head() { return 5.f; }
 // Floats of one unit's partial: [D + 2][BM], the outputs of a row down a
 // column, then its maximum and sum (lanes are rows, so both the writing warp
@@ -93,22 +93,22 @@ struct PrefixParams {
 struct PrefixPlan {
   int groups, per, own;
 };
-__device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams& x, int n_tiles, int n_ctas,
-                                                  float c_pair, float c_single, float c_tile) {
+__device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams& x, int n_steps, int n_ctas,
+                                                  float c_pair, float c_single, float c_step) {
   PrefixPlan r = {0, 0, 0};
   const int items = x.Hkv * x.nt;  // of one tile pair
   if (items > 0) {
     const bool single = x.rows - (x.pairs - 1) * 2 * px::BM <= px::BM;  // the last pair
     const float wa = static_cast<float>(items) *
                      (static_cast<float>(x.pairs - single) * c_pair + (single ? c_single : 0.f));
-    const float wb = static_cast<float>(n_tiles) * c_tile;
+    const float wb = static_cast<float>(n_steps) * c_step;
     // na with head + wa / na = wb / (n - na), where head is what a prefix CTA
     // takes besides its items
     const float n = static_cast<float>(n_ctas), h = px::cost_head();
     const float p = wa + wb - h * n;
-    int na = n_tiles == 0 ? n_ctas
+    int na = n_steps == 0 ? n_ctas
                           : static_cast<int>((sqrtf(p * p + 4.f * h * wa * n) - p) / (2.f * h) + 0.5f);
-    na = max(1, min(na, n_tiles > 0 ? n_ctas - 1 : n_ctas));
+    na = max(1, min(na, n_steps > 0 ? n_ctas - 1 : n_ctas));
     if (x.pairs <= na && (na / x.pairs) * x.pairs * 8 >= na * 7) {
       r.groups = x.pairs;
       r.per = min(na / x.pairs, items);
@@ -123,7 +123,7 @@ __device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams& x, int n_t
     const int over = r.per % heads;
     if (r.per > heads && over * 8 <= r.per) r.per -= over;
   }
-  r.own = min(n_tiles, n_ctas - r.groups * r.per);
+  r.own = min(n_steps, n_ctas - r.groups * r.per);
   return r;
 }
 
@@ -614,9 +614,11 @@ __device__ __forceinline__ void prefix_share(PrefixSmem<D>& s, const CUtensorMap
 }
 
 // The sequences' own rows.  A sequence here is (batch entry, K/V head, chunk of
-// up to 8 query heads); its rows are cut into tiles of 16, the tiles of all
-// sequences are numbered through, and every warp of every own CTA takes an even
-// share of them.  A warp feeds itself (its own ring of tiles, one lane issuing
+// up to 8 query heads); its rows are cut into tiles of 16.  A sequence of n tiles
+// counts n + 1 steps, the last of them empty: what starting and ending it takes
+// (without it a warp with a share of one-tile sequences took half as long again
+// as the others).  The steps of all sequences are numbered through, and every
+// warp of every own CTA takes an even share of them.  A warp feeds itself (its own ring of tiles, one lane issuing
 // the copies) and keeps the running softmax of its 16 keys x 8 heads in
 // registers, so no warp waits for another: with four warps of a block sharing
 // 64-row tiles and merging at the end of every sequence, 1024 sequences of 256
@@ -628,20 +630,24 @@ struct OwnSmem {
   alignas(1024) __nv_bfloat16 k[px::OW][px::OS][px::OT * D];
   alignas(1024) __nv_bfloat16 v[px::OW][px::OS][px::OT * D];
   uint64_t full[px::OW][px::OS];
-  int before[dec::MAX_BATCH + 1];  // tiles of a head chunk's sequences in the entries before b
+  int before[dec::MAX_BATCH + 1];  // steps of one sequence each of the entries before b
 };
 
-// before[b] = tiles of one sequence of each of the entries 0 .. b - 1, summed;
+// before[b] = steps of one sequence of each of the entries 0 .. b - 1, summed;
 // every thread of the block takes part.
 template <bool APPEND>
-__device__ __forceinline__ void scan_tiles(int* before, const PrefixParams& x) {
+__device__ __forceinline__ void scan_steps(int* before, const PrefixParams& x) {
   using namespace px;
+  auto steps = [&](int b) {
+    const int len = attend_len(x.lens[b], x.L, APPEND);
+    return len > 0 ? (len + OT - 1) / OT + 1 : 0;
+  };
   __shared__ int warp_total[THREADS / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (x.b + THREADS - 1) / THREADS;
   const int lo = min(x.b, static_cast<int>(threadIdx.x) * per), hi = min(x.b, lo + per);
   int sum = 0;
-  for (int b = lo; b < hi; ++b) sum += (attend_len(x.lens[b], x.L, APPEND) + OT - 1) / OT;
+  for (int b = lo; b < hi; ++b) sum += steps(b);
   int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -655,20 +661,21 @@ __device__ __forceinline__ void scan_tiles(int* before, const PrefixParams& x) {
   if (threadIdx.x == THREADS - 1) before[x.b] = acc + sum;
   for (int b = lo; b < hi; ++b) {
     before[b] = acc;
-    acc += (attend_len(x.lens[b], x.L, APPEND) + OT - 1) / OT;
+    acc += steps(b);
   }
   __syncthreads();
 }
 
-// A place in the list of tiles.
+// A tile's place in the list of steps.
 struct OwnCursor {
+  int i;             // its step
   int b, seq, c, n;  // batch entry, sequence within it, tile of that, its tiles
 };
 
 template <int D, bool APPEND>
 __device__ __forceinline__ void own_share(OwnSmem<D>& s, const CUtensorMap& tm_k,
                                           const CUtensorMap& tm_v, const PrefixParams& x,
-                                          int worker, int n_workers, int n_tiles) {
+                                          int worker, int n_workers, int n_steps) {
   using namespace px;
   constexpr int KSTEPS = D / 16;
   constexpr int CB = D / 64;
@@ -677,38 +684,59 @@ __device__ __forceinline__ void own_share(OwnSmem<D>& s, const CUtensorMap& tm_k
   const int g = lane >> 2, t = lane & 3;
   const int mat = lane >> 3, r8 = lane & 7;
   const int per_b = x.Hkv * x.hchunks;
-  const int x0 = static_cast<int>(share_start(worker, n_tiles, n_workers));
-  const int x1 = static_cast<int>(share_start(worker + 1, n_tiles, n_workers));
+  const int x1 = static_cast<int>(share_start(worker + 1, n_steps, n_workers));
 
-  OwnCursor at;  // of the tile in hand
-  {
-    int lo = 0, hi = x.b - 1;  // the largest b with before[b] * per_b <= x0
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s.before[mid] * per_b <= x0) lo = mid;
-      else hi = mid - 1;
-    }
-    at.b = lo;
-    at.n = s.before[lo + 1] - s.before[lo];
-    const int rest = x0 - s.before[lo] * per_b;
-    at.seq = rest / at.n;
-    at.c = rest - at.seq * at.n;
-  }
-  OwnCursor to = at;  // of the next tile to be fetched
+  // to the next tile, over the empty step and the entries without a row
   auto advance = [&](OwnCursor& u) {
+    ++u.i;
     if (++u.c < u.n) return;
+    ++u.i;
     u.c = 0;
     if (++u.seq < per_b) return;
     u.seq = 0;
     do ++u.b;
     while (u.b < x.b && s.before[u.b + 1] == s.before[u.b]);
-    u.n = u.b < x.b ? s.before[u.b + 1] - s.before[u.b] : 0;
+    u.n = u.b < x.b ? s.before[u.b + 1] - s.before[u.b] - 1 : 0;
   };
-  auto fetch = [&](int i) {  // tile i of the list, at the cursor `to`
-    const int st = (i - x0) % OS;
+  OwnCursor at;  // of the tile in hand
+  {
+    at.i = static_cast<int>(share_start(worker, n_steps, n_workers));
+    int lo = 0, hi = x.b - 1;  // the largest b with before[b] * per_b <= at.i
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s.before[mid] * per_b <= at.i) lo = mid;
+      else hi = mid - 1;
+    }
+    const int steps = s.before[lo + 1] - s.before[lo];
+    const int rest = at.i - s.before[lo] * per_b;
+    at.b = lo;
+    at.n = steps - 1;
+    at.seq = rest / steps;
+    at.c = rest - at.seq * steps;
+    if (at.c == at.n) {  // the share starts at an empty step
+      --at.i;
+      --at.c;
+      advance(at);
+    }
+  }
+  OwnCursor to = at;  // of the next tile to be fetched
+  int fetched = 0;
+  // the tile at `to`; with a sequence's first tile its query rows, with its last
+  // one the step's own row are brought to L2, so that a share of many short
+  // sequences does not pay for each from memory
+  auto fetch = [&]() {
+    const int st = fetched % OS;
+    const int kvh = to.seq / x.hchunks, hc = to.seq - kvh * x.hchunks;
+    const int bh = to.b * x.Hkv + kvh;
+    if (to.c == 0 && fetched > 0 && lane < 8 * CB && hc * 8 + lane / CB < x.group)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(
+          x.q + (static_cast<size_t>(to.b) * x.H + kvh * x.group + hc * 8 + lane / CB) * D +
+          lane % CB * 64));
+    if (APPEND && to.c + 1 == to.n && lane < 2 * CB)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(
+          (lane < CB ? x.k_new : x.v_new) + static_cast<size_t>(bh) * D + lane % CB * 64));
     if (elect_one()) {
       mbar_arrive_expect_tx(&s.full[warp][st], 2u * OT * D * 2u);
-      const int bh = to.b * x.Hkv + to.seq / x.hchunks;
 #pragma unroll
       for (int cb = 0; cb < CB; ++cb) {
         tma_load_3d(&s.k[warp][st][cb * OT * 64], &tm_k, &s.full[warp][st], cb * 64, to.c * OT, bh);
@@ -716,22 +744,24 @@ __device__ __forceinline__ void own_share(OwnSmem<D>& s, const CUtensorMap& tm_k
       }
     }
     __syncwarp();
+    ++fetched;
     advance(to);
   };
-  for (int i = x0; i < min(x0 + OS, x1); ++i) fetch(i);
+#pragma unroll 1
+  for (int k = 0; k < OS && to.i < x1; ++k) fetch();
 
   uint32_t qf[KSTEPS][2];
   float m_run[2], l_run[2], o[KSTEPS][4];
   bool home = false;
   int len = 0;
-  for (int i = x0; i < x1; ++i) {
-    const int st = (i - x0) % OS;
+  for (int k = 0; at.i < x1; ++k) {
+    const int st = k % OS;
     const int kvh = at.seq / x.hchunks, hc = at.seq - kvh * x.hchunks;
-    if (i == x0 || at.c == 0) {  // a segment starts
+    if (k == 0 || at.c == 0) {  // a segment starts
       home = at.c == 0;
       if (home) {
-        const int n = i + at.n <= x1 ? 1
-            : static_cast<int>(share_owner(i + at.n - 1, n_tiles, n_workers)) - worker + 1;
+        const int n = at.i + at.n <= x1 ? 1
+            : static_cast<int>(share_owner(at.i + at.n - 1, n_steps, n_workers)) - worker + 1;
         if (lane == 0) x.own_of[at.b * per_b + at.seq] = make_int2(worker, n);
       }
       len = attend_len(x.lens[at.b], x.L, APPEND);
@@ -749,19 +779,21 @@ __device__ __forceinline__ void own_share(OwnSmem<D>& s, const CUtensorMap& tm_k
 #pragma unroll
       for (int mt = 0; mt < KSTEPS; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
     }
-    if (!mbar_wait(&s.full[warp][st], static_cast<uint32_t>((i - x0) / OS) & 1)) return;
     const int n_valid = min(OT, len - at.c * OT);
+    const bool patch = APPEND && at.c == at.n - 1;  // the step's own row is the last
+    const size_t bh = static_cast<size_t>(at.b) * x.Hkv + kvh;
+    uint4 kn, vn;
+    if (patch && lane < D / 8) {  // (on their way while the tile is waited for)
+      kn = *reinterpret_cast<const uint4*>(x.k_new + bh * D + lane * 8);
+      vn = *reinterpret_cast<const uint4*>(x.v_new + bh * D + lane * 8);
+    }
+    if (!mbar_wait(&s.full[warp][st], static_cast<uint32_t>(k / OS) & 1)) return;
     uint8_t* kb = reinterpret_cast<uint8_t*>(&s.k[warp][st][0]);
     uint8_t* vb = reinterpret_cast<uint8_t*>(&s.v[warp][st][0]);
-    const bool patch = APPEND && at.c == at.n - 1;  // the step's own row is the last
     if (patch) {
-      const int r = n_valid - 1;
-      const size_t row = static_cast<size_t>(at.b) * x.Hkv + kvh;
-      const size_t crow = (row * x.L + (len - 1)) * D;
+      const size_t crow = (bh * x.L + (len - 1)) * D;
       if (lane < D / 8) {
-        const uint4 kn = *reinterpret_cast<const uint4*>(x.k_new + row * D + lane * 8);
-        const uint4 vn = *reinterpret_cast<const uint4*>(x.v_new + row * D + lane * 8);
-        const uint32_t off = (lane / 8) * BLOCK_BYTES + sw128_offset(r, lane % 8);
+        const uint32_t off = (lane / 8) * BLOCK_BYTES + sw128_offset(n_valid - 1, lane % 8);
         *reinterpret_cast<uint4*>(kb + off) = kn;
         *reinterpret_cast<uint4*>(vb + off) = vn;
         if (hc == 0) {
@@ -834,8 +866,8 @@ __device__ __forceinline__ void own_share(OwnSmem<D>& s, const CUtensorMap& tm_k
       mma_bf16_16816(o[mt], a0, a1, a2, a3, pb0, pb1);
     }
     __syncwarp();
-    if (i + OS < x1) fetch(i + OS);
-    if (i + 1 == x1 || at.c + 1 == at.n) {  // the segment ends: its partial
+    if (to.i < x1) fetch();
+    if (at.i + 1 >= x1 || at.c + 1 == at.n) {  // the segment ends: its partial
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 4);
@@ -886,11 +918,11 @@ __global__ void __launch_bounds__(px::THREADS, 1)
   OwnSmem<D>& own = *reinterpret_cast<OwnSmem<D>*>(smem);
   // a programmatic dependent of what precedes it: no global memory before this
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  scan_tiles<APPEND>(own.before, x);
-  const int n_tiles = own.before[x.b] * x.Hkv * x.hchunks;
+  scan_steps<APPEND>(own.before, x);
+  const int n_steps = own.before[x.b] * x.Hkv * x.hchunks;
   const PrefixPlan plan =
-      prefix_plan(x, n_tiles, gridDim.x, cost_pair(D), cost_single(D), cost_tile(D));
-  const int n_workers = min(n_tiles, plan.own * OW);
+      prefix_plan(x, n_steps, gridDim.x, cost_pair(D), cost_single(D), cost_step(D));
+  const int n_workers = min(n_steps, plan.own * OW);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // own CTAs evenly among the others, so that no part of the chip has only the
   // ones or the others on its way to memory
@@ -913,7 +945,7 @@ __global__ void __launch_bounds__(px::THREADS, 1)
     fence_mbar_init();
   }
   __syncwarp();
-  own_share<D, APPEND>(own, tm_k, tm_v, x, worker, n_workers, n_tiles);
+  own_share<D, APPEND>(own, tm_k, tm_v, x, worker, n_workers, n_steps);
 }
 
 // Merges the partials of 32 query rows of one K/V head: a lane is a row, a warp

@@ -461,7 +461,7 @@ int decode_prefix(const void* q, const void* k_new, const void* v_new, const voi
   // items and tiles are counted in 32 bits
   const long long seqs = static_cast<long long>(bsz) * Hkv * ((H / Hkv + 7) / 8);
   if (static_cast<long long>(w.pairs) * Hkv * w.nt > 0x7fffffffLL ||
-      seqs * (L / la::px::OT + 1) > 0x7fffffffLL)
+      seqs * (L / la::px::OT + 2) > 0x7fffffffLL)
     return LLAMA_ERR_UNSUPPORTED;
   CUtensorMap tkp{}, tvp{}, tk, tv;
   if (P > 0) {
