@@ -244,13 +244,23 @@ def _on(device: torch.device, where: str, fn, args, stream):
         raise LlamaAttnError(status, where)
 
 
+def _scratch(like: torch.Tensor, nbytes: int, stream) -> torch.Tensor:
+    """Scratch memory of the stream that will use it: once freed it may only be handed
+    to work that follows there."""
+    if stream is None:
+        return like.new_empty(nbytes, dtype=torch.uint8)
+    with torch.cuda.stream(stream):
+        return like.new_empty(nbytes, dtype=torch.uint8)
+
+
 def _table_scaled(where: str, pos: torch.Tensor, head_dim: int, args, stream):
-    fn = getattr(load(), where)
+    fn = getattr(_lib or load(), where)
     if pos.dtype is not torch.int64 or not pos.is_contiguous():
-        pos = pos.to(torch.int64).contiguous()
+        with torch.cuda.stream(stream):  # (None: no change) where the kernel reads it
+            pos = pos.to(torch.int64).contiguous()
     p = _ptr(pos)
     shape, dev = pos.shape, pos.device
-    cos = torch.empty((*shape, head_dim), device=dev, dtype=torch.float32)
+    cos = pos.new_empty((*shape, head_dim), dtype=torch.float32)
     sin = torch.empty_like(cos)
     bsz = shape[0] if len(shape) > 1 else 1
     _on(dev, where, fn, (p, bsz, pos.numel() // max(bsz, 1), head_dim, *args, cos.data_ptr(),
@@ -306,7 +316,7 @@ def rope_apply(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, si
     (parts of a fused projection), and so may out, a pair of tensors (q and k themselves:
     in place; k's: rows of a cache).  transpose: the gradient of the rotation."""
     w = "llama_rope_apply"
-    fn = load().llama_rope_apply
+    fn = (_lib or load()).llama_rope_apply
     shape, dev, dt = q.shape, q.device, q.dtype
     if len(shape) == 4:
         b, s, H, D = shape
@@ -320,10 +330,13 @@ def rope_apply(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, si
         raise ValueError(f"{w}: cos and sin must have one shape")
     qp, qs = _rope_view(q, w, "q", dt, dev, shape)
     q_out, k_out = out if out is not None else (None, None)
+    qos = kp = ks = kop = kos = None  # (strides of an output made here: dense)
+    Hkv = 0
     if q_out is None:
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    qop, qos = _rope_view(q_out, w, "out", dt, dev, shape)
-    Hkv, kp, ks, kop, kos = 0, None, None, None, None
+        qop = q_out.data_ptr()
+    else:
+        qop, qos = _rope_view(q_out, w, "out", dt, dev, shape)
     if k is not None:
         k_shape = k.shape
         if k_shape[:-2] != shape[:-2] or k_shape[-1] != D:
@@ -332,7 +345,9 @@ def rope_apply(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, si
         kp, ks = _rope_view(k, w, "k", dt, dev, k_shape)
         if k_out is None:
             k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-        kop, kos = _rope_view(k_out, w, "out", dt, dev, k_shape)
+            kop = k_out.data_ptr()
+        else:
+            kop, kos = _rope_view(k_out, w, "out", dt, dev, k_shape)
     elif k_out is not None:
         raise ValueError(f"{w}: an output for k needs k")
     _on(dev, w, fn, (qp, kp, _ptr(cos), _ptr(sin), b, s, H, Hkv, D, R, 1 if interleaved else 0,
@@ -615,18 +630,17 @@ def decode_prefix_workspace_bytes(bsz, n_heads, n_kv_heads, prefix_len, head_dim
                                                                head_dim))
 
 
-def _prefix_view(t: torch.Tensor, name: str, like: torch.Tensor, Hkv: int, P: int, D: int):
+def _prefix_view(t: torch.Tensor, name: str, P: int, D: int):
     """(pointer, strides of K/V head and row) of a prefix tensor [Hkv, P, D]."""
-    w = "llama_attn_decode_prefix"
     if not t.is_cuda:
         raise ValueError("llama_attn: tensors must live on a CUDA device")
-    _need(t, w, name, like.dtype, like.device, (Hkv, P, D))
     head, row, one = t.stride()
     if one != 1:
-        raise ValueError(f"{w}: the dimensions of a row of {name} must be adjacent")
+        raise ValueError("llama_attn_decode_prefix: the dimensions of a row of "
+                         f"{name} must be adjacent")
     # the stride of an extent of one is never used; torch leaves it arbitrary
     row = row if P > 1 else D
-    return t.data_ptr(), _PrefixStrides(head if Hkv > 1 else P * row, row)
+    return t.data_ptr(), _PrefixStrides(head if t.shape[0] > 1 else P * row, row)
 
 
 def decode_prefix(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor,
@@ -639,37 +653,33 @@ def decode_prefix(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tenso
     cache_lens int32 [b] -> out [b, H*D].  With k_new, v_new [b,Hkv,D] (k_new rotated)
     the step's own row is appended to the caches first."""
     w = "llama_attn_decode_prefix"
-    fn = load().llama_attn_decode_prefix
+    fn = (_lib or load()).llama_attn_decode_prefix
     b, H, D = q.shape
-    Hkv, L = k_cache.shape[1], k_cache.shape[2]
+    _, Hkv, L, _ = k_cache.shape
     P = k_prefix.shape[1]
-    dev = q.device
-    dt = q.dtype
-    _need(k_cache, w, "k_cache", dt, dev, (b, Hkv, L, D))
-    _need(v_cache, w, "v_cache", dt, dev, (b, Hkv, L, D))
+    dev, dt = q.device, q.dtype
+    new = (b, Hkv, D)
+    for t, name, shape in ((k_cache, "k_cache", (b, Hkv, L, D)), (v_cache, "v_cache", (b, Hkv, L, D)),
+                           (k_prefix, "k_prefix", (Hkv, P, D)), (v_prefix, "v_prefix", (Hkv, P, D)),
+                           (k_new, "k_new", new), (v_new, "v_new", new)):
+        if t is not None and (t.shape != shape or t.dtype is not dt or t.device != dev):
+            _need(t, w, name, dt, dev, shape)
     _need(cache_lens, w, "cache_lens", torch.int32, dev, None, b)
-    kn = vn = None
-    if k_new is not None:
-        _need(k_new, w, "k_new", dt, dev, (b, Hkv, D))
-        kn = _ptr(k_new)
-    if v_new is not None:
-        _need(v_new, w, "v_new", dt, dev, (b, Hkv, D))
-        vn = _ptr(v_new)
     _need(out, w, "out", dt, dev, None, b * H * D)
-    kp, ks = _prefix_view(k_prefix, "k_prefix", q, Hkv, P, D)
-    vp, vs = _prefix_view(v_prefix, "v_prefix", q, Hkv, P, D)
+    kp, ks = _prefix_view(k_prefix, "k_prefix", P, D)
+    vp, vs = _prefix_view(v_prefix, "v_prefix", P, D)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty((b, H * D), device=dev, dtype=dt)
-    if workspace is None:  # (this call's own: torch hands it over, nothing to check)
+        out = q.new_empty((b, H * D))
+    if workspace is None:
         need = decode_prefix_workspace_bytes(b, H, Hkv, P, D)
-        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+        workspace = _scratch(q, need, stream)
         ws, ws_bytes = workspace.data_ptr(), need
     else:
         ws, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
-    _on(dev, w, fn, (_ptr(q), kn, vn, kp, vp, P, ks, vs, _ptr(k_cache), _ptr(v_cache),
-                     _ptr(cache_lens), b, H, Hkv, L, D, scale, _ptr(out), ws, ws_bytes,
+    _on(dev, w, fn, (_ptr(q), _ptr(k_new), _ptr(v_new), kp, vp, P, ks, vs, _ptr(k_cache),
+                     _ptr(v_cache), _ptr(cache_lens), b, H, Hkv, L, D, scale, _ptr(out), ws, ws_bytes,
                      _dtype_code(dt)), stream)
     return out
 

@@ -68,8 +68,8 @@ constexpr int OT = 16;
 struct PrefixParams {
   const __nv_bfloat16* q;  // [b, H, D]
   float* part;             // prefix partials [tile pairs * Hkv + MAX_CTAS][2][D + 2][BM]
-  float* own_home;         // [b, H, D + 4]: an own segment from its sequence's first row
-  float* own_mid;          // [MAX_CTAS * OW][8, D + 4]: a worker's segment from inside one
+  float* own_home;         // [b * Hkv * hchunks][D + 2][heads]: from a sequence's first row
+  float* own_mid;          // [MAX_CTAS * OW][D + 2][heads]: a worker's segment from inside one
   int2* part_of;           // [tile pairs * Hkv] CTA with the home slot, segments
   int2* own_of;            // [b * Hkv * hchunks] worker with the home slot, segments
   int rows;                // query rows of a K/V head: b * group
@@ -78,6 +78,7 @@ struct PrefixParams {
   int pairs;               // tile pairs: ceil(rows / 256)
   int b, H, Hkv, L, group;
   int hchunks;             // ceil(group / 8)
+  int heads;               // min(group, 8), the heads of a chunk's partial
   const int* lens;             // [b]
   const __nv_bfloat16* k_new;  // [b, Hkv, D] or null
   const __nv_bfloat16* v_new;
@@ -874,22 +875,20 @@ __device__ __forceinline__ void own_share(OwnSmem<D>& s, const CUtensorMap& tm_k
         l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 8);
         l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 16);
       }
+      float* dst = (home ? x.own_home + static_cast<size_t>(at.b * per_b + at.seq) * (D + 2) * x.heads
+                         : x.own_mid + static_cast<size_t>(worker) * (D + 2) * x.heads) +
+                   2 * t;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int hh = 2 * t + h;
-        if (hc * 8 + hh < x.group) {
-          float* dst = home
-              ? x.own_home + (static_cast<size_t>(at.b) * x.H + kvh * x.group + hc * 8 + hh) *
-                                 dec::part_stride(D)
-              : x.own_mid + (static_cast<size_t>(worker) * 8 + hh) * dec::part_stride(D);
+        if (hc * 8 + 2 * t + h < x.group) {
 #pragma unroll
           for (int mt = 0; mt < KSTEPS; ++mt) {
-            dst[mt * 16 + g] = o[mt][h];
-            dst[mt * 16 + g + 8] = o[mt][h + 2];
+            dst[(mt * 16 + g) * x.heads + h] = o[mt][h];
+            dst[(mt * 16 + g + 8) * x.heads + h] = o[mt][h + 2];
           }
           if (g == 0) {
-            dst[D] = m_run[h];
-            dst[D + 1] = l_run[h];
+            dst[D * x.heads + h] = m_run[h];
+            dst[(D + 1) * x.heads + h] = l_run[h];
           }
         }
       }
@@ -950,19 +949,21 @@ __global__ void __launch_bounds__(px::THREADS, 1)
 
 // Merges the partials of 32 query rows of one K/V head: a lane is a row, a warp
 // 8 of its dimensions, and WK warps with the same dimensions take the partials
-// in turn and are merged through shared memory.  Four partials are loaded at a
-// time.
+// in turn and are merged through shared memory.  Bound by the latency of its
+// loads: U = 2 partials at a time in 64 registers, which lets four blocks into an
+// SM, was faster than U = 4 with three (35.0 against 36.3 us for 32 sequences behind
+// 8192 tokens).
 namespace px {
 constexpr int COMBINE_WARPS = 8;
 }
 template <int D, int WK>
-__global__ void __launch_bounds__(px::COMBINE_WARPS * 32, 3)
+__global__ void __launch_bounds__(px::COMBINE_WARPS * 32, 4)
     decode_prefix_combine_kernel(const __grid_constant__ PrefixParams x, int append,
                                  __nv_bfloat16* __restrict__ out) {
   using namespace px;
   constexpr int WD = COMBINE_WARPS / WK;  // warps side by side over the dimensions
   constexpr int DC = D / (8 * WD);        // blocks over the dimensions
-  constexpr int U = 4;
+  constexpr int U = 2;  // partials loaded at a time
   __shared__ float so[COMBINE_WARPS][10][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int wk = warp / WD, wd = warp - wk * WD;
@@ -977,10 +978,11 @@ __global__ void __launch_bounds__(px::COMBINE_WARPS * 32, 3)
   const int pair = row0 / (2 * BM), in_pair = row0 - pair * 2 * BM;
   const bool single = x.rows - pair * 2 * BM <= BM;
   const int seq = pair * x.Hkv + kvh;
+  const int own_seq = (b * x.Hkv + kvh) * x.hchunks + h / 8;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int2 pre = x.nt > 0 ? x.part_of[seq] : make_int2(0, 0);
-  int2 own = x.own_of[(b * x.Hkv + kvh) * x.hchunks + h / 8];
+  int2 own = x.own_of[own_seq];
   if (attend_len(x.lens[b], x.L, append) == 0) own = make_int2(0, 0);  // (nothing was noted)
 
   float m = -INFINITY, l = 0.f, o[8];
@@ -1005,43 +1007,34 @@ __global__ void __launch_bounds__(px::COMBINE_WARPS * 32, 3)
     }
     m = top;
   };
-  // ---- prefix: the home slot, then those of the CTAs that follow its CTA; two
-  // units each if they share their rows
-  const int n_pre = pre.y << single;
+  // the partials: of the prefix the home slot, then those of the CTAs that follow
+  // its CTA, two units each if they share their rows; of the own rows the home
+  // slot, then those of the workers that follow.  A column of each holds one row.
+  const int n_pre = pre.y << single, n = n_pre + own.y;
   const float* base = x.part + in_pair / BM * unit_floats(D) + in_pair % BM + lane;
-  for (int k0 = wk; k0 < n_pre; k0 += U * WK) {
+  for (int k0 = wk; k0 < n; k0 += U * WK) {
     float mc[U], lc[U], oc[U][8];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = k0 + u * WK;
-      const int seg = k >> single;
-      const int slot = seg == 0 ? seq : x.pairs * x.Hkv + pre.x + seg;
-      const float* src = base + static_cast<long long>(2 * slot + (single ? k & 1 : 0)) * unit_floats(D);
-      const bool there = valid && k < n_pre;
-      mc[u] = there ? src[D * BM] : -INFINITY;
-      lc[u] = there ? src[(D + 1) * BM] : 0.f;
+      const float* src;
+      int stride = BM;
+      if (k < n_pre) {
+        const int seg = k >> single;
+        const int slot = seg == 0 ? seq : x.pairs * x.Hkv + pre.x + seg;
+        src = base + static_cast<long long>(2 * slot + (single ? k & 1 : 0)) * unit_floats(D);
+      } else {
+        const int seg = k - n_pre;
+        const long long slot = seg == 0 ? own_seq : own.x + seg;
+        stride = x.heads;
+        src = (seg == 0 ? x.own_home : x.own_mid) + slot * (D + 2) * stride + h % 8;
+      }
+      const bool there = valid && k < n;
+      mc[u] = there ? src[D * stride] : -INFINITY;
+      lc[u] = there ? src[(D + 1) * stride] : 0.f;
+      src += d0 * stride;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) oc[u][e] = there ? src[(d0 + e) * BM] : 0.f;
-    }
-    add(mc, lc, oc);
-  }
-  // ---- own rows: the home slot, then those of the workers that follow
-  for (int k0 = (wk + WK - n_pre % WK) % WK; k0 < own.y; k0 += U * WK) {
-    float mc[U], lc[U], oc[U][8];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = k0 + u * WK;
-      const float* src = k == 0
-          ? x.own_home + (static_cast<size_t>(b) * x.H + kvh * x.group + h) * dec::part_stride(D)
-          : x.own_mid + (static_cast<size_t>(own.x + k) * 8 + h % 8) * dec::part_stride(D);
-      const bool there = k < own.y;
-      const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-      const float4 a = there ? *reinterpret_cast<const float4*>(src + d0) : z;
-      const float4 c = there ? *reinterpret_cast<const float4*>(src + d0 + 4) : z;
-      const float2 ml = there ? *reinterpret_cast<const float2*>(src + D) : make_float2(-INFINITY, 0.f);
-      mc[u] = ml.x, lc[u] = ml.y;
-      oc[u][0] = a.x, oc[u][1] = a.y, oc[u][2] = a.z, oc[u][3] = a.w;
-      oc[u][4] = c.x, oc[u][5] = c.y, oc[u][6] = c.z, oc[u][7] = c.w;
+      for (int e = 0; e < 8; ++e) oc[u][e] = there ? src[e * stride] : 0.f;
     }
     add(mc, lc, oc);
   }

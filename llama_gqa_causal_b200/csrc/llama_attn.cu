@@ -438,11 +438,13 @@ PrefixLayout prefix_layout(int bsz, int H, int Hkv, int P, int D) {
   const size_t seqs = static_cast<size_t>(w.pairs) * Hkv;
   const size_t slots = w.nt == 0 ? 0 : seqs + std::min<size_t>(seqs * w.nt, MAX_CTAS);
   w.home = up(slots * 2 * unit_floats(D) * sizeof(float));
-  const size_t row = la::dec::part_stride(D) * sizeof(float);
-  w.mid = w.home + up(static_cast<size_t>(bsz) * H * row);
-  w.part_of = w.mid + up(static_cast<size_t>(MAX_CTAS) * OW * 8 * row);
+  const int group = H / Hkv;
+  const size_t chunks = static_cast<size_t>(bsz) * Hkv * ((group + 7) / 8);
+  const size_t chunk = static_cast<size_t>(D + 2) * std::min(group, 8) * sizeof(float);
+  w.mid = w.home + up(chunks * chunk);
+  w.part_of = w.mid + up(static_cast<size_t>(MAX_CTAS) * OW * chunk);
   w.own_of = w.part_of + up(seqs * sizeof(int2));
-  w.bytes = w.own_of + up(static_cast<size_t>(bsz) * Hkv * ((H / Hkv + 7) / 8) * sizeof(int2));
+  w.bytes = w.own_of + up(chunks * sizeof(int2));
   return w;
 }
 
@@ -499,6 +501,7 @@ int decode_prefix(const void* q, const void* k_new, const void* v_new, const voi
   x.L = L;
   x.group = H / Hkv;
   x.hchunks = (x.group + 7) / 8;
+  x.heads = std::min(x.group, 8);
   x.lens = lens;
   x.k_new = static_cast<const __nv_bfloat16*>(k_new);
   x.v_new = static_cast<const __nv_bfloat16*>(v_new);
@@ -518,7 +521,7 @@ int decode_prefix(const void* q, const void* k_new, const void* v_new, const voi
                          "prefix decode", tkp, tvp, tk, tv, x);
   }
   if (e) return e;
-  // the combine kernel's blocks in one wave (three to an SM): the fewer rows there
+  // the combine kernel's blocks in one wave (four to an SM): the fewer rows there
   // are, the more warps share the partials of one
   const long long row_blocks = (static_cast<long long>(x.rows) + 31) / 32 * Hkv;
   auto combine = [&](auto wk) {
@@ -527,7 +530,7 @@ int decode_prefix(const void* q, const void* k_new, const void* v_new, const voi
                             la::px::COMBINE_WARPS * 32, 0, st, "prefix combine", x, append,
                             static_cast<__nv_bfloat16*>(out));
   };
-  const long long fit = 3LL * n_ctas / (row_blocks * (D / 64));
+  const long long fit = 4LL * n_ctas / (row_blocks * (D / 64));
   if (fit >= 8) return combine(std::integral_constant<int, 8>{});
   if (fit >= 4) return combine(std::integral_constant<int, 4>{});
   if (fit >= 2) return combine(std::integral_constant<int, 2>{});
