@@ -164,6 +164,12 @@ __device__ __forceinline__ void exp2_cubic2(float& y0, float& y1, float x0, floa
   y1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
 }
 
+// share_start in 32 bits: i n / g = i (n / g) + i (n % g) / g, for g^2 < 2^31.
+__device__ __forceinline__ int share_begin(int i, int n, int g) {
+  const int each = n / g;
+  return i * each + i * (n - each * g) / g;
+}
+
 // A run of items inside one (tile pair, K/V head).
 struct PrefixSegment {
   int seq, kvh;   // seq = tile pair * Hkv + kvh
@@ -200,8 +206,8 @@ __device__ __forceinline__ void prefix_share(PrefixSmem<D>& s, const CUtensorMap
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int items = x.Hkv * x.nt * (x.pairs / plan.groups);  // of this CTA's group
   const int group = cta / plan.per, in_group = cta - group * plan.per;
-  const int x0 = group * items + static_cast<int>(share_start(in_group, items, plan.per));
-  const int x1 = group * items + static_cast<int>(share_start(in_group + 1, items, plan.per));
+  const int x0 = group * items + share_begin(in_group, items, plan.per);
+  const int x1 = group * items + share_begin(in_group + 1, items, plan.per);
 
   // ---- Q rows into a unit's tile, by its softmax warps: row m of the K/V head
   // is batch entry m / group, head kvh * group + m % group; a row's 16-byte
@@ -685,7 +691,7 @@ __device__ __forceinline__ void own_share(OwnSmem<D>& s, const CUtensorMap& tm_k
   const int g = lane >> 2, t = lane & 3;
   const int mat = lane >> 3, r8 = lane & 7;
   const int per_b = x.Hkv * x.hchunks;
-  const int x1 = static_cast<int>(share_start(worker + 1, n_steps, n_workers));
+  const int x1 = share_begin(worker + 1, n_steps, n_workers);
 
   // to the next tile, over the empty step and the entries without a row
   auto advance = [&](OwnCursor& u) {
@@ -701,7 +707,7 @@ __device__ __forceinline__ void own_share(OwnSmem<D>& s, const CUtensorMap& tm_k
   };
   OwnCursor at;  // of the tile in hand
   {
-    at.i = static_cast<int>(share_start(worker, n_steps, n_workers));
+    at.i = share_begin(worker, n_steps, n_workers);
     int lo = 0, hi = x.b - 1;  // the largest b with before[b] * per_b <= at.i
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -917,6 +923,12 @@ __global__ void __launch_bounds__(px::THREADS, 1)
   OwnSmem<D>& own = *reinterpret_cast<OwnSmem<D>*>(smem);
   // a programmatic dependent of what precedes it: no global memory before this
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  {
+    // q to L2 while the lengths are read: where its rows go is only known then
+    const size_t line = static_cast<size_t>(blockIdx.x) * THREADS + threadIdx.x;
+    if (line < static_cast<size_t>(x.b) * x.H * D / 64)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(x.q + line * 64));
+  }
   scan_steps<APPEND>(own.before, x);
   const int n_steps = own.before[x.b] * x.Hkv * x.hchunks;
   const PrefixPlan plan =

@@ -549,11 +549,14 @@ int rope_table_scaled(const long long* pos, int bsz, int seq, int head_dim, doub
   // enough blocks to fill the GPU eight times over at most: a thread then
   // walks its rows with the frequencies it has loaded
   const long long blocks = std::min<long long>((n + rows - 1) / rows, 148LL * 8);
+  // a table that fills half of L2 or more is written past it (131072 rows of 128:
+  // 26.7 us through it, 21.8 past it); a smaller one is left there for its reader
+  const bool stream_out = n * head_dim * 8 >= (64LL << 20);
   if (vec)
     return launch_dependent(la::rope_table_scaled_kernel<4>, blocks, rows * per_row, 0, st,
-                            "scaled rope table", pos, n, half, gain, cos, sin, freqs);
+                            "scaled rope table", pos, n, half, gain, stream_out, cos, sin, freqs);
   return launch_dependent(la::rope_table_scaled_kernel<1>, blocks, rows * per_row, 0, st,
-                          "scaled rope table", pos, n, half, gain, cos, sin, freqs);
+                          "scaled rope table", pos, n, half, gain, stream_out, cos, sin, freqs);
 }
 
 int check_table_scaled(const long long* pos, int bsz, int seq, int head_dim, double theta,

@@ -58,7 +58,8 @@ __device__ __forceinline__ void sincos_reduced(double x, float& s, float& c) {
 template <int VEC>
 __global__ void __launch_bounds__(ra::THREADS)
     rope_table_scaled_kernel(const long long* __restrict__ pos, long long n_rows, int half,
-                             double gain, float* __restrict__ cos_out, float* __restrict__ sin_out,
+                             double gain, bool stream_out, float* __restrict__ cos_out,
+                             float* __restrict__ sin_out,
                              const __grid_constant__ ScaledFreqs freqs) {
   const int per_row = half / VEC;
   const int rows_per_block = blockDim.x / per_row;
@@ -93,10 +94,17 @@ __global__ void __launch_bounds__(ra::THREADS)
     float* so = sin_out + r * 2 * half + i;
     if constexpr (VEC == 4) {
       const float4 cv = make_float4(c[0], c[1], c[2], c[3]), sv = make_float4(s[0], s[1], s[2], s[3]);
-      *reinterpret_cast<float4*>(co) = cv;
-      *reinterpret_cast<float4*>(co + half) = cv;
-      *reinterpret_cast<float4*>(so) = sv;
-      *reinterpret_cast<float4*>(so + half) = sv;
+      if (stream_out) {
+        __stcs(reinterpret_cast<float4*>(co), cv);
+        __stcs(reinterpret_cast<float4*>(co + half), cv);
+        __stcs(reinterpret_cast<float4*>(so), sv);
+        __stcs(reinterpret_cast<float4*>(so + half), sv);
+      } else {
+        *reinterpret_cast<float4*>(co) = cv;
+        *reinterpret_cast<float4*>(co + half) = cv;
+        *reinterpret_cast<float4*>(so) = sv;
+        *reinterpret_cast<float4*>(so + half) = sv;
+      }
     } else {
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
