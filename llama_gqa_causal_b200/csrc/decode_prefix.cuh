@@ -52,9 +52,9 @@ constexpr int kPolyPairsOf8 = 1;  // pairs of 8 exponentiated on the FMA pipe
 // Work of an item and of a step through the own rows (16 of them), in units that only their
 // ratios matter of: what one SM takes for it.
 __host__ __device__ constexpr float cost_pair(int d) { return d == 128 ? 2.1f : 1.5f; }
-__host__ __device__ constexpr float cost_single(int d) { return d == 128 ? 1.2f : 0.8f; }
+__host__ __device__ constexpr float cost_single(int d) { return d == 128 ? 1.6f : 1.1f; }
 __host__ __device__ constexpr float cost_step(int d) { return d == 128 ? 0.12f : 0.07f; }
-__host__ __device__ constexpr float cost_head() { return 5.f; }
+__host__ __device__ constexpr float cost_head(int d) { return d == 128 ? 8.f : 4.f; }
 // Floats of one unit's partial: [D + 2][BM], the outputs of a row down a
 // column, then its maximum and sum (lanes are rows, so both the writing warp
 // and the combining one touch whole lines).
@@ -95,7 +95,8 @@ struct PrefixPlan {
   int groups, per, own;
 };
 __device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams& x, int n_steps, int n_ctas,
-                                                  float c_pair, float c_single, float c_step) {
+                                                  float c_pair, float c_single, float c_step,
+                                                  float c_head) {
   PrefixPlan r = {0, 0, 0};
   const int items = x.Hkv * x.nt;  // of one tile pair
   if (items > 0) {
@@ -105,10 +106,11 @@ __device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams& x, int n_s
     const float wb = static_cast<float>(n_steps) * c_step;
     // na with head + wa / na = wb / (n - na), where head is what a prefix CTA
     // takes besides its items
-    const float n = static_cast<float>(n_ctas), h = px::cost_head();
-    const float p = wa + wb - h * n;
-    int na = n_steps == 0 ? n_ctas
-                          : static_cast<int>((sqrtf(p * p + 4.f * h * wa * n) - p) / (2.f * h) + 0.5f);
+    const float n = static_cast<float>(n_ctas), h = c_head;
+    const float p = wa + wb - h * n, root = sqrtf(p * p + 4.f * h * wa * n);
+    int na = n_ctas;
+    if (n_steps > 0)  // (either form of the root, so that nothing cancels)
+      na = static_cast<int>((p > 0.f ? 2.f * wa * n / (p + root) : (root - p) / (2.f * h)) + 0.5f);
     na = max(1, min(na, n_steps > 0 ? n_ctas - 1 : n_ctas));
     if (x.pairs <= na && (na / x.pairs) * x.pairs * 8 >= na * 7) {
       r.groups = x.pairs;
@@ -932,7 +934,8 @@ __global__ void __launch_bounds__(px::THREADS, 1)
   scan_steps<APPEND>(own.before, x);
   const int n_steps = own.before[x.b] * x.Hkv * x.hchunks;
   const PrefixPlan plan =
-      prefix_plan(x, n_steps, gridDim.x, cost_pair(D), cost_single(D), cost_step(D));
+      prefix_plan(x, n_steps, gridDim.x, cost_pair(D), cost_single(D), cost_step(D),
+                  cost_head(D));
   const int n_workers = min(n_steps, plan.own * OW);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // own CTAs evenly among the others, so that no part of the chip has only the
