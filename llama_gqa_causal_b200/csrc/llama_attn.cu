@@ -448,6 +448,27 @@ PrefixLayout prefix_layout(int bsz, int H, int Hkv, int P, int D) {
   return w;
 }
 
+// Whether a block is to take a whole sequence, prefix included: by what either
+// way takes, in microseconds, with the caches taken for half full (their fill is
+// known on the device alone).  A block has some 2.5 and 5.5 a thousand rows, in
+// waves of the blocks that fit; the split has 11 to 13 for two launches and the
+// merge, 1 (heads of 64: 0.6) a thousand query rows, and its work over the SMs.
+// Measured from 32 to 1024 sequences and 20 to 4000 rows, the faster way is taken
+// but for cases within 15% of each other.
+bool prefix_one_block(int bsz, int H, int Hkv, int P, int L, int D, long long seqs,
+                      const PrefixLayout& w, int n_ctas) {
+  using namespace la::px;
+  const double wide = D == 128 ? 1.0 : 0.6;
+  const long long fit = static_cast<long long>(n_ctas) * (D == 128 ? 1 : 2);
+  const double waves = static_cast<double>((seqs + fit - 1) / fit);
+  const double rows = 0.5 * L;
+  const double one = waves * (2.5 + 0.0055 * (P + rows));
+  const double split = 10.5 + 2.0 * wide + 1e-3 * wide * bsz * H +
+                       (static_cast<double>(w.pairs) * Hkv * (cost_segment(D) + cost_pair(D) * w.nt) +
+                        seqs * rows / OT * cost_step(D)) / n_ctas;
+  return one < split;
+}
+
 constexpr long long kMaxPrefixStride = 1LL << 39;  // of a tensor map: 2^40 bytes
 
 static_assert(la::prefix_smem_bytes<128>() + 64 <= 227 * 1024 &&
@@ -465,13 +486,16 @@ int decode_prefix(const void* q, const void* k_new, const void* v_new, const voi
   if (static_cast<long long>(w.pairs) * Hkv * w.nt > 0x7fffffffLL ||
       seqs * (L / la::px::OT + 2) > 0x7fffffffLL)
     return LLAMA_ERR_UNSUPPORTED;
+  const int n_ctas = std::min(sm_count(), la::px::MAX_CTAS);
+  if (n_ctas <= 1) return LLAMA_ERR_CUDA;
+  const bool small = prefix_one_block(bsz, H, Hkv, P, L, D, seqs, w, n_ctas);
   CUtensorMap tkp{}, tvp{}, tk, tv;
   if (P > 0) {
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(P),
                                 static_cast<cuuint64_t>(Hkv)};
     const cuuint64_t kst[2] = {static_cast<cuuint64_t>(ks[1]) * 2, static_cast<cuuint64_t>(ks[0]) * 2};
     const cuuint64_t vst[2] = {static_cast<cuuint64_t>(vs[1]) * 2, static_cast<cuuint64_t>(vs[0]) * 2};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(la::px::BN), 1};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(small ? la::px::OT : la::px::BN), 1};
     if (!make_map(&tkp, k_prefix, 3, dims, kst, box)) return LLAMA_ERR_CUDA;
     if (!make_map(&tvp, v_prefix, 3, dims, vst, box)) return LLAMA_ERR_CUDA;
   }
@@ -481,8 +505,6 @@ int decode_prefix(const void* q, const void* k_new, const void* v_new, const voi
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(la::px::OT), 1};
   if (!make_map(&tk, k_cache, 3, dims, strides, box)) return LLAMA_ERR_CUDA;
   if (!make_map(&tv, v_cache, 3, dims, strides, box)) return LLAMA_ERR_CUDA;
-  const int n_ctas = std::min(sm_count(), la::px::MAX_CTAS);
-  if (n_ctas <= 1) return LLAMA_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   la::PrefixParams x;
   x.q = static_cast<const __nv_bfloat16*>(q);
@@ -508,8 +530,20 @@ int decode_prefix(const void* q, const void* k_new, const void* v_new, const voi
   x.k_cache = static_cast<__nv_bfloat16*>(k_cache);
   x.v_cache = static_cast<__nv_bfloat16*>(v_cache);
   x.scale_log2 = scale * 1.4426950408889634f;
-  constexpr size_t smem = la::prefix_smem_bytes<D>();
   const int append = k_new != nullptr;
+  if (small) {
+    constexpr size_t smem = sizeof(la::SmallSmem<D>) + 1024;
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
+    if (append) {
+      if (!ensure_smem_attr<la::decode_prefix_small_kernel<D, true>>(smem)) return LLAMA_ERR_CUDA;
+      return launch_dependent(la::decode_prefix_small_kernel<D, true>, seqs,
+                              la::px::SMALL_WARPS * 32, smem, st, "prefix decode", tkp, tvp, tk, tv, x, o);
+    }
+    if (!ensure_smem_attr<la::decode_prefix_small_kernel<D, false>>(smem)) return LLAMA_ERR_CUDA;
+    return launch_dependent(la::decode_prefix_small_kernel<D, false>, seqs, la::px::SMALL_WARPS * 32,
+                            smem, st, "prefix decode", tkp, tvp, tk, tv, x, o);
+  }
+  constexpr size_t smem = la::prefix_smem_bytes<D>();
   int e;
   if (append) {
     if (!ensure_smem_attr<la::decode_prefix_kernel<D, true>>(smem)) return LLAMA_ERR_CUDA;
