@@ -61,6 +61,7 @@ __host__ __device__ constexpr float cost_segment(int d) { return d == 128 ? 4.f 
 __host__ __device__ constexpr int unit_floats(int d) { return (d + 2) * BM; }
 // Own rows: warps of a CTA, stages of a warp, rows of a tile.
 constexpr int OW = THREADS / 32;
+__host__ __device__ constexpr int ow_min(int d) { return d == 128 ? 6 : 9; }
 constexpr int OS = 2;
 constexpr int OT = 16;
 }  // namespace px
@@ -965,7 +966,14 @@ __global__ void __launch_bounds__(px::THREADS, 1)
   const PrefixPlan plan =
       prefix_plan(x, n_steps, gridDim.x, cost_pair(D), cost_single(D), cost_step(D),
                   cost_segment(D));
-  const int n_workers = min(n_steps, plan.own * OW);
+  // warps of an own CTA: all 12, or as many as make ow_min a CTA of the whole
+  // chip.  Reads under way from more places than that make memory slower: 32
+  // sequences of 4096 own rows, 146 own CTAs, 117 us with 12 warps, 90 with 6
+  // (heads of 64, half the bytes a tile: 59 with 12, 55 with 8, 68 with 6); with
+  // 68 own CTAs beside the prefix's, 8 warps were 6% slower than 12.
+  const int own_warps =
+      plan.own > 0 ? min(OW, max(ow_min(D), ow_min(D) * MAX_CTAS / plan.own)) : OW;
+  const int n_workers = min(n_steps, plan.own * own_warps);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // own CTAs evenly among the others, so that no part of the chip has only the
   // ones or the others on its way to memory

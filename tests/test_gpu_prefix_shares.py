@@ -132,3 +132,40 @@ def test_a_row_of_queries_far_from_the_others():
     # scores of entry 7 reach some 50: 66 products and sums of 2^-24 each of 50, twice in
     # numerator and denominator, 4e-4 relative: under 2^-11 of the mean of |v|, four times
     assert (err[7] <= tol[7] + 2.0 ** -9 * x["v_prefix"].abs().max().double()).all()
+
+
+@pytest.mark.parametrize("append", [False, True], ids=["plain", "append"])
+@pytest.mark.parametrize("P", [1, 63, 128, 129, 257])
+@pytest.mark.parametrize("shape", [(40, 32, 32, 128), (40, 96, 32, 128), (64, 32, 32, 64),
+                                   (70, 160, 8, 64), (150, 56, 8, 128)],
+                         ids=lambda s: "b%dH%dK%dD%d" % s)
+def test_many_sequences_behind_a_short_prefix(shape, P, append):
+    """So many that they are split over the SMs, with few tiles of the prefix: groups of 1,
+    3, 7 and 20 heads, tile pairs shared and full, segments of one tile."""
+    b, H, Hkv, D = shape
+    lens = [(0, 3, 1, 17, 16, 2)[i % 6] for i in range(b)]
+    x = inputs(b, H, Hkv, D, P, 17, lens, seed=P + b, append=append)
+    before = {k: v.clone() for k, v in x.items() if "cache" in k}
+    out = run(x)
+    want, tol, kc, vc = expected(dict(x, k_cache=before["k_cache"], v_cache=before["v_cache"]))
+    assert ((out.double() - want).abs() <= tol).all()
+    for name, was in (("k_cache", kc), ("v_cache", vc)):
+        assert torch.equal(x[name].view(torch.int16), was.view(torch.int16))
+
+
+def test_a_large_batch_with_nan_where_nothing_is_attended_and_where_it_is():
+    b, Hkv = 40, 32
+    x = inputs(b, 32, Hkv, 128, 200, 17, [i % 18 for i in range(b)], seed=9)
+    clean = run(x).view(b, 32, 128)
+    x["q"][11, 5, 0] = float("nan")
+    x["v_cache"][17, 3, 16, 7] = float("nan")
+    x["k_cache"][16, 2, 3, 1] = float("nan")
+    out = run(x).view(b, 32, 128)
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[11, 5] = bad[16, 2] = True
+    bad[17, 3, 7] = True
+    assert out[bad].isnan().all() and torch.equal(out[~bad], clean[~bad])
+    x["k_prefix"][4, 199, 3] = float("nan")
+    out = run(x).view(b, 32, 128)
+    bad[:, 4] = True
+    assert out[bad].isnan().all() and torch.equal(out[~bad], clean[~bad])
