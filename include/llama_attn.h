@@ -408,7 +408,10 @@ int llama_attn_decode_noalloc(const void* q, const void* k_cache, const void* v_
  *   out[b, h] = softmax(scale * q[b, h] . [K_prefix; K_b]) [V_prefix; V_b],
  * in one softmax over both.  The prefix is held and read once for the whole
  * batch: its products are taken for all query rows of a K/V head together, and
- * merged with each sequence's own part by the log-sum-exp identity.
+ * merged with each sequence's own part by the log-sum-exp identity (a small batch
+ * with little behind it is done sequence by sequence in one launch instead; which
+ * way is taken depends on the sizes alone).  Scores, softmax statistics and sums
+ * are fp32; the probabilities are rounded to bf16 before the product with V.
  *   q          [bsz, n_heads, head_dim], already rotated (llama_attn_qkv_rope or
  *              llama_rope_apply)
  *   k_new, v_new  [bsz, n_kv_heads, head_dim] the step's own key (already
@@ -430,8 +433,9 @@ int llama_attn_decode_noalloc(const void* q, const void* k_cache, const void* v_
  *              llama_attn_decode_prefix_workspace_bytes(...) bytes
  * prefix_len is a host value: the prefix is fixed while its batch decodes.
  * bf16 only.  Errors: as llama_attn_decode, plus INVALID_ARG for one of k_new
- * and v_new alone, prefix_len < 0, a prefix stride that is not a multiple of 8
- * or is less than head_dim, and UNSUPPORTED for fp32.
+ * and v_new alone, prefix_len < 0, a prefix stride that is not a multiple of 8,
+ * is less than head_dim or is 2^39 or more, and UNSUPPORTED for fp32, for bsz >
+ * 4096 and for sizes whose tiles cannot be counted in 31 bits.
  */
 int llama_attn_decode_prefix(const void* q, const void* k_new, const void* v_new,
                              const void* k_prefix, const void* v_prefix, int prefix_len,

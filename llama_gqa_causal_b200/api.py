@@ -658,29 +658,40 @@ def decode_prefix(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tenso
     _, Hkv, L, _ = k_cache.shape
     P = k_prefix.shape[1]
     dev, dt = q.device, q.dtype
-    new = (b, Hkv, D)
-    for t, name, shape in ((k_cache, "k_cache", (b, Hkv, L, D)), (v_cache, "v_cache", (b, Hkv, L, D)),
-                           (k_prefix, "k_prefix", (Hkv, P, D)), (v_prefix, "v_prefix", (Hkv, P, D)),
+    cache, prefix, new = (b, Hkv, L, D), (Hkv, P, D), (b, Hkv, D)
+    for t, name, shape in ((k_cache, "k_cache", cache), (v_cache, "v_cache", cache),
+                           (k_prefix, "k_prefix", prefix), (v_prefix, "v_prefix", prefix),
                            (k_new, "k_new", new), (v_new, "v_new", new)):
         if t is not None and (t.shape != shape or t.dtype is not dt or t.device != dev):
             _need(t, w, name, dt, dev, shape)
-    _need(cache_lens, w, "cache_lens", torch.int32, dev, None, b)
-    _need(out, w, "out", dt, dev, None, b * H * D)
+    if cache_lens.dtype is not torch.int32 or cache_lens.device != dev or cache_lens.numel() != b:
+        _need(cache_lens, w, "cache_lens", torch.int32, dev, None, b)
+    if out is not None:
+        _need(out, w, "out", dt, dev, None, b * H * D)
+    ptr = []
+    for t in (q, k_new, v_new, k_cache, v_cache, cache_lens):  # (all on q's device)
+        if t is None:
+            ptr.append(None)
+        else:
+            ptr.append(t.data_ptr() if t.is_contiguous() and dev.type == "cuda" else _ptr(t))
     kp, ks = _prefix_view(k_prefix, "k_prefix", P, D)
     vp, vs = _prefix_view(v_prefix, "v_prefix", P, D)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
         out = q.new_empty((b, H * D))
+        op = out.data_ptr()
+    else:
+        op = _ptr(out)
     if workspace is None:
         need = decode_prefix_workspace_bytes(b, H, Hkv, P, D)
         workspace = _scratch(q, need, stream)
         ws, ws_bytes = workspace.data_ptr(), need
     else:
         ws, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
-    _on(dev, w, fn, (_ptr(q), _ptr(k_new), _ptr(v_new), kp, vp, P, ks, vs, _ptr(k_cache),
-                     _ptr(v_cache), _ptr(cache_lens), b, H, Hkv, L, D, scale, _ptr(out), ws, ws_bytes,
-                     _dtype_code(dt)), stream)
+    qp, knp, vnp, kcp, vcp, lp = ptr
+    _on(dev, w, fn, (qp, knp, vnp, kp, vp, P, ks, vs, kcp, vcp, lp, b, H, Hkv, L, D, scale, op, ws,
+                     ws_bytes, _dtype_code(dt)), stream)
     return out
 
 

@@ -27,6 +27,15 @@
 // and MMA issuer, warps 4-7 and 8-11 the softmax of unit 0 and 1 (a thread per
 // query row = TMEM lane).  TMEM: S_0, S_1 (128 columns each; P overwrites S),
 // O_0, O_1 (D each).
+//
+// What bounds it: the prefix part's full tile pairs, like the prefill's tiles, the
+// chain S -> softmax -> P -> P V -> S of either unit, which the other unit's half
+// hides (a pair's 128 keys take 1.85 us an SM, 1.1 PFLOP/s over the chip; the
+// tensor pipe is busy 53 % of the time); shared tile pairs and the own rows,
+// memory.  32 sequences behind 8192 keys with 512 own rows on average (64/8 heads
+// of 128, caches cold): 32 us for 102 MB; 128 behind 32768: 140 us for 139 GFLOP.
+// Few sequences with little behind them are taken whole by a block each
+// (decode_prefix_small_kernel), which saves the second launch and the partials.
 #pragma once
 #include <type_traits>
 
@@ -48,9 +57,13 @@ static_assert(kRegsControl % 8 == 0 && kRegsSoftmax % 8 == 0, "setmaxnreg takes 
 static_assert(kRegsControl + 2 * kRegsSoftmax <= 3 * kRegsAtLaunch,
               "setmaxnreg split exceeds the registers the block is launched with");
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr int kPolyPairsOf8 = 1;  // pairs of 8 exponentiated on the FMA pipe
-// Work of an item and of a step through the own rows (16 of them), in units that only their
-// ratios matter of: what one SM takes for it.
+// Pairs of 8 exponentiated on the FMA pipe instead of the MUFU: 0, 1 and 2 took
+// 127, 123.5 and 123.5 us for 128 sequences behind 32768 keys.
+constexpr int kPolyPairsOf8 = 1;
+// What one SM takes, in microseconds as a batch of 16 to 128 sequences ran, for
+// an item of a full and of a shared tile pair, a segment's beginning and end (Q,
+// the pipeline's fill, the partial's write), and a step through the own rows.
+// Only their ratios matter.
 __host__ __device__ constexpr float cost_pair(int d) { return d == 128 ? 2.1f : 1.5f; }
 __host__ __device__ constexpr float cost_single(int d) { return d == 128 ? 1.6f : 1.1f; }
 __host__ __device__ constexpr float cost_step(int d) { return d == 128 ? 0.12f : 0.07f; }
