@@ -324,6 +324,8 @@ def rope_apply(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, si
         b, (s, H, D) = 1, shape
     else:
         raise ValueError(f"{w}: q must be [b, s, heads, head_dim] or [s, heads, head_dim]")
+    if cos is None or sin is None:
+        raise ValueError(f"{w}: pass both cos and sin")
     R = cos.shape[-1]
     _tables(cos, sin, w, dev, b * s, R)
     if sin.shape != cos.shape:

@@ -759,9 +759,9 @@ struct Tiles16 {
 // counts n + 1 steps, the last of them empty: what starting and ending it takes
 // (without it a warp with a share of one-tile sequences took half as long again
 // as the others).  The steps of all sequences are numbered through, and every
-// warp of every own CTA takes an even share of them.  A warp feeds itself (its own ring of tiles, one lane issuing
-// the copies) and keeps the running softmax of its 16 keys x 8 heads in
-// registers, so no warp waits for another: with four warps of a block sharing
+// warp of every own CTA takes an even share of them.  A warp feeds itself (its
+// own ring of tiles, one lane issuing the copies) and keeps its running softmax
+// in registers, so no warp waits for another: with four warps of a block sharing
 // 64-row tiles and merging at the end of every sequence, 1024 sequences of 256
 // rows ran at 2.7 TB/s.
 template <int D>
@@ -912,7 +912,12 @@ __device__ __forceinline__ void own_share(OwnSmem<D>& s, const CUtensorMap& tm_k
       kn = *reinterpret_cast<const uint4*>(x.k_new + bh * D + lane * 8);
       vn = *reinterpret_cast<const uint4*>(x.v_new + bh * D + lane * 8);
     }
-    if (!mbar_wait(&s.full[warp][st], static_cast<uint32_t>(k / OS) & 1)) return;
+    if (!mbar_wait(&s.full[warp][st], static_cast<uint32_t>(k / OS) & 1)) {
+      // (given up: the status word is set; leave no copy in flight)
+      for (int j = k; j < fetched; ++j)
+        mbar_wait(&s.full[warp][j % OS], static_cast<uint32_t>(j / OS) & 1);
+      return;
+    }
     uint8_t* kb = reinterpret_cast<uint8_t*>(&s.k[warp][st][0]);
     uint8_t* vb = reinterpret_cast<uint8_t*>(&s.v[warp][st][0]);
     if (patch && hc == 0 && lane < D / 8) {
@@ -1221,6 +1226,8 @@ __global__ void __launch_bounds__(px::SMALL_WARPS * 32)
   for (int i = warp, k = 0; i < n; i += W, ++k) {
     const int st = k % OS;
     if (!mbar_wait(&s.full[warp][st], static_cast<uint32_t>(k / OS) & 1)) {
+      for (int j = k; j < fetched; ++j)  // (given up: leave no copy in flight)
+        mbar_wait(&s.full[warp][j % OS], static_cast<uint32_t>(j / OS) & 1);
       ok = false;
       break;
     }
@@ -1230,7 +1237,10 @@ __global__ void __launch_bounds__(px::SMALL_WARPS * 32)
     t16.fix(kb, vb, n_valid, APPEND && i == n - 1, kn, vn);
     t16.add(kb, vb, n_valid, x.scale_log2);
     __syncwarp();
-    if (i + OS * W < n) fetch(i + OS * W, st);
+    if (i + OS * W < n) {
+      fetch(i + OS * W, st);
+      ++fetched;
+    }
   }
   if (mine && hc == 0 && ok) {
     const size_t crow = (static_cast<size_t>(bh) * x.L + (len - 1)) * D + lane * 8;

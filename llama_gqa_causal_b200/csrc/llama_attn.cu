@@ -607,8 +607,9 @@ int check_table_scaled(const long long* pos, int bsz, int seq, int head_dim, dou
 constexpr double kPi = 3.14159265358979323846;
 
 // Fills in one tensor of a rotation; false for strides that are negative, that
-// differ between a tensor and itself as the output, or that make two output elements one (checked with the extents in the order of
-// their strides, each of which has to step over all that lies below it).
+// differ between a tensor and itself as the output, or that make two output
+// elements one (checked with the extents in the order of their strides, each of
+// which has to step over all that lies below it).
 bool rope_side(la::RopeSide* sd, const void* x, const long long* xs, void* y, const long long* ys,
                int bsz, int seq, int heads, int D) {
   sd->x = x;
