@@ -101,23 +101,20 @@ struct PrefixParams {
   float scale_log2;
 };
 
-// How the CTAs are dealt out.  The prefix's items are split over groups of
-// `per` CTAs: one group per tile pair, so that the CTAs of different tile pairs
-// read the same keys at about the same time, or one group for everything where
-// whole groups would leave more than an eighth of the prefix's CTAs idle.
+// How many CTAs take a share of the prefix's items, and how many of the own rows.
 struct PrefixPlan {
-  int groups, per, own;
+  int prefix, own;
 };
 __device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams& x, int n_steps, int n_ctas,
                                                   float c_pair, float c_single, float c_step,
                                                   float c_segment) {
-  PrefixPlan r = {0, 0, 0};
-  const int items = x.Hkv * x.nt;  // of one tile pair
-  if (items > 0) {
+  PrefixPlan r = {0, 0};
+  const int runs = x.pairs * x.Hkv;  // of x.nt items
+  if (x.nt > 0) {
     const bool single = x.rows - (x.pairs - 1) * 2 * px::BM <= px::BM;  // the last pair
-    const float wa = static_cast<float>(x.pairs * x.Hkv) * c_segment +
-                     static_cast<float>(items) *
-                         (static_cast<float>(x.pairs - single) * c_pair + (single ? c_single : 0.f));
+    const float per_head = static_cast<float>(x.pairs - single) * c_pair + (single ? c_single : 0.f);
+    const float wa = static_cast<float>(runs) * c_segment +
+                     static_cast<float>(x.Hkv) * static_cast<float>(x.nt) * per_head;
     const float wb = static_cast<float>(n_steps) * c_step;
     // na with h + wa / na = wb / (n - na), where h is what a prefix CTA takes
     // besides its items and their segments (a split one among them) more than an
@@ -128,21 +125,14 @@ __device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams& x, int n_s
     if (n_steps > 0)  // (either form of the root, so that nothing cancels)
       na = static_cast<int>((p > 0.f ? 2.f * wa * n / (p + root) : (root - p) / (2.f * h)) + 0.5f);
     na = max(1, min(na, n_steps > 0 ? n_ctas - 1 : n_ctas));
-    if (x.pairs <= na && (na / x.pairs) * x.pairs * 8 >= na * 7) {
-      r.groups = x.pairs;
-      r.per = min(na / x.pairs, items);
-    } else {
-      r.groups = 1;
-      r.per = min(na, items * x.pairs);
-    }
-    // whole CTAs to every K/V head of a group where that idles (or, if there are
-    // own rows to be had, hands over) few: a CTA with one segment is done sooner
-    // than one that turns from one head to the next
-    const int heads = x.Hkv * (x.pairs / r.groups);
-    const int over = r.per % heads;
-    if (r.per > heads && over * 8 <= r.per) r.per -= over;
+    r.prefix = min(na, runs * x.nt);
+    // whole CTAs to every run where that hands over few to the own rows (or idles
+    // few): a CTA with one segment is done sooner than one that turns from one
+    // run to the next (32 sequences behind 8192 keys 33.0 -> 31.3 us)
+    const int over = r.prefix % runs;
+    if (r.prefix > runs && over * 8 <= r.prefix) r.prefix -= over;
   }
-  r.own = min(n_steps, n_ctas - r.groups * r.per);
+  r.own = min(n_steps, n_ctas - r.prefix);
   return r;
 }
 
@@ -212,7 +202,7 @@ __device__ __forceinline__ PrefixSegment prefix_segment(const PrefixParams& x, i
 template <int D>
 __device__ __forceinline__ void prefix_share(PrefixSmem<D>& s, const CUtensorMap& tm_k,
                                              const CUtensorMap& tm_v, const PrefixParams& x,
-                                             const PrefixPlan& plan, int cta) {
+                                             int cta, int n_ctas) {
   using namespace px;
   constexpr int CB = D / 64;                  // 64-column swizzle blocks per row
   constexpr int NST = ring(D);
@@ -222,10 +212,8 @@ __device__ __forceinline__ void prefix_share(PrefixSmem<D>& s, const CUtensorMap
   constexpr uint32_t IDESC_PV = idesc_bf16(BM, D, true);
   constexpr uint32_t TMEM_COLS = 512;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int items = x.Hkv * x.nt * (x.pairs / plan.groups);  // of this CTA's group
-  const int group = cta / plan.per, in_group = cta - group * plan.per;
-  const int x0 = group * items + share_begin(in_group, items, plan.per);
-  const int x1 = group * items + share_begin(in_group + 1, items, plan.per);
+  const int items = x.pairs * x.Hkv * x.nt;
+  const int x0 = share_begin(cta, items, n_ctas), x1 = share_begin(cta + 1, items, n_ctas);
 
   // ---- Q rows into a unit's tile, by its softmax warps: row m of the K/V head
   // is batch entry m / group, head kvh * group + m % group; a row's 16-byte
@@ -447,11 +435,9 @@ __device__ __forceinline__ void prefix_share(PrefixSmem<D>& s, const CUtensorMap
     if (warp == 2 && lane == 0)
       for (int i = x0; i < x1;) {
         const PrefixSegment g = prefix_segment(x, i, x1);
-        if (g.j0 == 0) {
-          const int end = i + x.nt - 1 - group * items;
-          x.part_of[g.seq] = make_int2(
-              cta, group * plan.per + static_cast<int>(share_owner(end, items, plan.per)) - cta + 1);
-        }
+        if (g.j0 == 0)
+          x.part_of[g.seq] =
+              make_int2(cta, static_cast<int>(share_owner(i + x.nt - 1, items, n_ctas)) - cta + 1);
         i += g.n;
       }
   } else {
@@ -999,11 +985,11 @@ __global__ void __launch_bounds__(px::THREADS, 1)
   const int own_before = blockIdx.x * plan.own / n;
   if ((blockIdx.x + 1) * plan.own / n == own_before) {
     const int cta = blockIdx.x - own_before;
-    if (cta >= plan.groups * plan.per) return;
+    if (cta >= plan.prefix) return;
     // the scan's shared memory has been read, and the ring's copies may land there
     fence_proxy_async_smem();
     __syncthreads();
-    prefix_share<D>(*reinterpret_cast<PrefixSmem<D>*>(smem), tm_kp, tm_vp, x, plan, cta);
+    prefix_share<D>(*reinterpret_cast<PrefixSmem<D>*>(smem), tm_kp, tm_vp, x, cta, plan.prefix);
     return;
   }
   // warps of one CTA are workers plan.own apart, so that few tiles spread over the SMs
