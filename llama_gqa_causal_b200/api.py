@@ -327,8 +327,9 @@ def rope_apply(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, si
     if cos is None or sin is None:
         raise ValueError(f"{w}: pass both cos and sin")
     R = cos.shape[-1]
-    _tables(cos, sin, w, dev, b * s, R)
-    if sin.shape != cos.shape:
+    if not (cos.dtype is sin.dtype is torch.float32 and cos.device == sin.device == dev
+            and cos.shape == sin.shape and cos.numel() == b * s * R):
+        _tables(cos, sin, w, dev, b * s, R)
         raise ValueError(f"{w}: cos and sin must have one shape")
     qp, qs = _rope_view(q, w, "q", dt, dev, shape)
     q_out, k_out = out if out is not None else (None, None)
@@ -661,21 +662,22 @@ def decode_prefix(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tenso
     P = k_prefix.shape[1]
     dev, dt = q.device, q.dtype
     cache, prefix, new = (b, Hkv, L, D), (Hkv, P, D), (b, Hkv, D)
-    for t, name, shape in ((k_cache, "k_cache", cache), (v_cache, "v_cache", cache),
-                           (k_prefix, "k_prefix", prefix), (v_prefix, "v_prefix", prefix),
-                           (k_new, "k_new", new), (v_new, "v_new", new)):
-        if t is not None and (t.shape != shape or t.dtype is not dt or t.device != dev):
+    # (one test of what fits; what does not is named by the checks that raise)
+    if not (k_cache.shape == v_cache.shape == cache and k_prefix.shape == v_prefix.shape == prefix
+            and k_cache.dtype is v_cache.dtype is k_prefix.dtype is v_prefix.dtype is dt
+            and k_cache.device == v_cache.device == k_prefix.device == v_prefix.device == dev):
+        for t, name, shape in ((k_cache, "k_cache", cache), (v_cache, "v_cache", cache),
+                               (k_prefix, "k_prefix", prefix), (v_prefix, "v_prefix", prefix)):
             _need(t, w, name, dt, dev, shape)
+    _need(k_new, w, "k_new", dt, dev, new)
+    _need(v_new, w, "v_new", dt, dev, new)
+    _need(out, w, "out", dt, dev, None, b * H * D)
     if cache_lens.dtype is not torch.int32 or cache_lens.device != dev or cache_lens.numel() != b:
         _need(cache_lens, w, "cache_lens", torch.int32, dev, None, b)
-    if out is not None:
-        _need(out, w, "out", dt, dev, None, b * H * D)
-    ptr = []
-    for t in (q, k_new, v_new, k_cache, v_cache, cache_lens):  # (all on q's device)
-        if t is None:
-            ptr.append(None)
-        else:
-            ptr.append(t.data_ptr() if t.is_contiguous() and dev.type == "cuda" else _ptr(t))
+    if not (q.is_cuda and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and cache_lens.is_contiguous()):
+        for t in (q, k_cache, v_cache, cache_lens):
+            _ptr(t)
     kp, ks = _prefix_view(k_prefix, "k_prefix", P, D)
     vp, vs = _prefix_view(v_prefix, "v_prefix", P, D)
     if scale is None:
@@ -691,8 +693,8 @@ def decode_prefix(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tenso
         ws, ws_bytes = workspace.data_ptr(), need
     else:
         ws, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
-    qp, knp, vnp, kcp, vcp, lp = ptr
-    _on(dev, w, fn, (qp, knp, vnp, kp, vp, P, ks, vs, kcp, vcp, lp, b, H, Hkv, L, D, scale, op, ws,
+    _on(dev, w, fn, (q.data_ptr(), _ptr(k_new), _ptr(v_new), kp, vp, P, ks, vs, k_cache.data_ptr(),
+                     v_cache.data_ptr(), cache_lens.data_ptr(), b, H, Hkv, L, D, scale, op, ws,
                      ws_bytes, _dtype_code(dt)), stream)
     return out
 
