@@ -1130,27 +1130,27 @@ __global__ void __launch_bounds__(px::COMBINE_WARPS * 32, 4)
   }
 }
 
-// Few sequences with little behind them: a block takes one sequence (batch entry,
-// K/V head, chunk of up to 8 query heads) from beginning to end, its warps the
+// Sequences with little behind them: a block takes one sequence (batch entry, K/V
+// head, chunk of up to 8 query heads) from beginning to end, its W warps the
 // 16-row tiles of prefix and own rows in turn, each through a ring of its own,
 // and merges them through shared memory.  One launch and no partials, but each
 // block reads the prefix for itself (out of L2, mostly) and a long one makes it
 // late.  The warps read rows that lie next to one another, and 144 sequences of
 // 4000 own rows run at 6.5 TB/s.  16 sequences x 8 K/V heads behind 500 + 100
 // rows: 6.1 us, against 14.9 split over the SMs; behind 3000 + 100: 17.4, 17.8.
-namespace px {
-constexpr int SMALL_WARPS = 8;
-}
-template <int D>
+// W = 8 where a wave of such blocks (166 KB of shared memory, 81 KB for heads of
+// 64) holds all sequences, else 4, of which two (five) fit an SM: 1024 sequences
+// behind 20 rows 10.8 us against 18.3, but 144 behind 1000 12.6 against 9.4.
+template <int D, int W>
 struct SmallSmem {
-  alignas(1024) __nv_bfloat16 k[px::SMALL_WARPS][px::OS][px::OT * D];
-  alignas(1024) __nv_bfloat16 v[px::SMALL_WARPS][px::OS][px::OT * D];
-  float o[px::SMALL_WARPS][8][D + 4];  // (+ 4 spreads the rows over the banks)
-  float m[px::SMALL_WARPS][8], l[px::SMALL_WARPS][8];
-  uint64_t full[px::SMALL_WARPS][px::OS];
+  alignas(1024) __nv_bfloat16 k[W][px::OS][px::OT * D];
+  alignas(1024) __nv_bfloat16 v[W][px::OS][px::OT * D];
+  float o[W][8][D + 4];  // (+ 4 spreads the rows over the banks)
+  float m[W][8], l[W][8];
+  uint64_t full[W][px::OS];
 };
-template <int D, bool APPEND>
-__global__ void __launch_bounds__(px::SMALL_WARPS * 32)
+template <int D, bool APPEND, int W>
+__global__ void __launch_bounds__(W * 32)
     decode_prefix_small_kernel(const __grid_constant__ CUtensorMap tm_kp,
                                const __grid_constant__ CUtensorMap tm_vp,
                                const __grid_constant__ CUtensorMap tm_k,
@@ -1159,9 +1159,8 @@ __global__ void __launch_bounds__(px::SMALL_WARPS * 32)
                                __nv_bfloat16* __restrict__ out) {
   using namespace px;
   constexpr int CB = D / 64;
-  constexpr int W = SMALL_WARPS;
   extern __shared__ uint8_t smem_raw[];
-  SmallSmem<D>& s = *reinterpret_cast<SmallSmem<D>*>(
+  SmallSmem<D, W>& s = *reinterpret_cast<SmallSmem<D, W>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per_b = x.Hkv * x.hchunks;
@@ -1249,26 +1248,27 @@ __global__ void __launch_bounds__(px::SMALL_WARPS * 32)
     }
   }
   __syncthreads();
-  if (warp >= n_heads) return;  // a warp a head
   constexpr int VEC = D / 32;
-  float top = -INFINITY, sum = 0.f, acc[VEC];
+  for (int hd = warp; hd < n_heads; hd += W) {
+    float top = -INFINITY, sum = 0.f, acc[VEC];
 #pragma unroll
-  for (int w = 0; w < W; ++w) top = fmax3_nan(top, s.m[w][warp], s.m[w][warp]);
-  const float ref = top == -INFINITY ? 0.f : top;
+    for (int w = 0; w < W; ++w) top = fmax3_nan(top, s.m[w][hd], s.m[w][hd]);
+    const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+    for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
 #pragma unroll
-  for (int w = 0; w < W; ++w) {
-    const float f = ex2_approx(s.m[w][warp] - ref);
-    sum = fmaf(f, s.l[w][warp], sum);
+    for (int w = 0; w < W; ++w) {
+      const float f = ex2_approx(s.m[w][hd] - ref);
+      sum = fmaf(f, s.l[w][hd], sum);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) acc[e] = fmaf(f, s.o[w][warp][lane * VEC + e], acc[e]);
+      for (int e = 0; e < VEC; ++e) acc[e] = fmaf(f, s.o[w][hd][lane * VEC + e], acc[e]);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    __nv_bfloat16* dst = out + (row0 + hd) * D + lane * VEC;
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  __nv_bfloat16* dst = out + (row0 + warp) * D + lane * VEC;
-#pragma unroll
-  for (int e = 0; e < VEC; e += 2)
-    *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
 }
 
 }  // namespace la

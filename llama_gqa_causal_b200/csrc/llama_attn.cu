@@ -448,25 +448,43 @@ PrefixLayout prefix_layout(int bsz, int H, int Hkv, int P, int D) {
   return w;
 }
 
-// Whether a block is to take a whole sequence, prefix included: by what either
-// way takes, in microseconds, with the caches taken for half full (their fill is
-// known on the device alone).  A block has some 2.5 and 5.5 a thousand rows, in
-// waves of the blocks that fit; the split has 11 to 13 for two launches and the
-// merge, 1 (heads of 64: 0.6) a thousand query rows, and its work over the SMs.
-// Measured from 32 to 1024 sequences and 20 to 4000 rows, the faster way is taken
-// but for cases within 15% of each other.
-bool prefix_one_block(int bsz, int H, int Hkv, int P, int L, int D, long long seqs,
-                      const PrefixLayout& w, int n_ctas) {
+// Warps of a block that takes a whole sequence, prefix included, or 0 for the
+// split over the SMs: by what either way takes, in microseconds, with the caches
+// taken for half full (their fill is known on the device alone).  A block of 8
+// warps has 2.5 and 5.5 a thousand rows.  Blocks of 4 have 2.5 and either 11.5 a
+// thousand rows or, where an SM has several sequences, 1.1 (heads of 64: 0.5) for
+// each of them and 6.2 (3.2) a thousand of their rows.  The split has 11 to 13 for
+// two launches and the merge, 1 (0.6) a thousand query rows, 0.03 (0.015) for each
+// CTA that leaves a partial of 256 rows, and its work over the SMs.  Measured
+// both ways from 8 to 1024 sequences and 20 to 4000 rows (208 sizes): the way
+// taken was the faster one or within 20% of it, but for one at 31%.
+int prefix_block_warps(int bsz, int H, int Hkv, int P, int L, int D, long long seqs,
+                       const PrefixLayout& w, int n_ctas) {
   using namespace la::px;
-  const double wide = D == 128 ? 1.0 : 0.6;
-  const long long fit = static_cast<long long>(n_ctas) * (D == 128 ? 1 : 2);
-  const double waves = static_cast<double>((seqs + fit - 1) / fit);
-  const double rows = 0.5 * L;
-  const double one = waves * (2.5 + 0.0055 * (P + rows));
-  const double split = 10.5 + 2.0 * wide + 1e-3 * wide * bsz * H +
-                       (static_cast<double>(w.pairs) * Hkv * (cost_segment(D) + cost_pair(D) * w.nt) +
-                        seqs * rows / OT * cost_step(D)) / n_ctas;
-  return one < split;
+  const bool wide = D == 128;
+  const double own = 0.5 * L, rows = P + own, n = n_ctas;
+  const int warps = seqs <= (wide ? n_ctas : 2 * n_ctas) ? 8 : 4;
+  const double block =
+      2.5 + (warps == 8 ? 0.0055 * rows
+                        : std::max(0.0115 * rows, seqs / n * (wide ? 1.1 + 0.0062 * rows
+                                                                   : 0.5 + 0.0032 * rows)));
+  const double q_rows = static_cast<double>(bsz) * (H / Hkv), runs = static_cast<double>(w.pairs) * Hkv;
+  const double item = q_rows <= BM ? cost_single(D) : cost_pair(D);
+  const double split =
+      (wide ? 12.5 : 11.7) + (wide ? 1e-3 : 6e-4) * bsz * H +
+      (wide ? 0.03 : 0.015) * std::min(n, runs * w.nt) * std::min(1.0, q_rows / (2 * BM)) +
+      (runs * (w.nt > 0 ? cost_segment(D) : 0.f) + runs * w.nt * item + seqs * own / OT * cost_step(D)) / n;
+  return block < split ? warps : 0;
+}
+
+template <int D, bool APPEND, int W>
+int decode_prefix_small(const CUtensorMap& tkp, const CUtensorMap& tvp, const CUtensorMap& tk,
+                        const CUtensorMap& tv, const la::PrefixParams& x, void* out,
+                        long long seqs, cudaStream_t st) {
+  constexpr size_t smem = sizeof(la::SmallSmem<D, W>) + 1024;
+  if (!ensure_smem_attr<la::decode_prefix_small_kernel<D, APPEND, W>>(smem)) return LLAMA_ERR_CUDA;
+  return launch_dependent(la::decode_prefix_small_kernel<D, APPEND, W>, seqs, W * 32, smem, st,
+                          "prefix decode", tkp, tvp, tk, tv, x, static_cast<__nv_bfloat16*>(out));
 }
 
 constexpr long long kMaxPrefixStride = 1LL << 39;  // of a tensor map: 2^40 bytes
@@ -488,7 +506,7 @@ int decode_prefix(const void* q, const void* k_new, const void* v_new, const voi
     return LLAMA_ERR_UNSUPPORTED;
   const int n_ctas = std::min(sm_count(), la::px::MAX_CTAS);
   if (n_ctas <= 1) return LLAMA_ERR_CUDA;
-  const bool small = prefix_one_block(bsz, H, Hkv, P, L, D, seqs, w, n_ctas);
+  const int small = prefix_block_warps(bsz, H, Hkv, P, L, D, seqs, w, n_ctas);
   CUtensorMap tkp{}, tvp{}, tk, tv;
   if (P > 0) {
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(P),
@@ -531,18 +549,12 @@ int decode_prefix(const void* q, const void* k_new, const void* v_new, const voi
   x.v_cache = static_cast<__nv_bfloat16*>(v_cache);
   x.scale_log2 = scale * 1.4426950408889634f;
   const int append = k_new != nullptr;
-  if (small) {
-    constexpr size_t smem = sizeof(la::SmallSmem<D>) + 1024;
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
-    if (append) {
-      if (!ensure_smem_attr<la::decode_prefix_small_kernel<D, true>>(smem)) return LLAMA_ERR_CUDA;
-      return launch_dependent(la::decode_prefix_small_kernel<D, true>, seqs,
-                              la::px::SMALL_WARPS * 32, smem, st, "prefix decode", tkp, tvp, tk, tv, x, o);
-    }
-    if (!ensure_smem_attr<la::decode_prefix_small_kernel<D, false>>(smem)) return LLAMA_ERR_CUDA;
-    return launch_dependent(la::decode_prefix_small_kernel<D, false>, seqs, la::px::SMALL_WARPS * 32,
-                            smem, st, "prefix decode", tkp, tvp, tk, tv, x, o);
-  }
+  if (small == 8)
+    return append ? decode_prefix_small<D, true, 8>(tkp, tvp, tk, tv, x, out, seqs, st)
+                  : decode_prefix_small<D, false, 8>(tkp, tvp, tk, tv, x, out, seqs, st);
+  if (small == 4)
+    return append ? decode_prefix_small<D, true, 4>(tkp, tvp, tk, tv, x, out, seqs, st)
+                  : decode_prefix_small<D, false, 4>(tkp, tvp, tk, tv, x, out, seqs, st);
   constexpr size_t smem = la::prefix_smem_bytes<D>();
   int e;
   if (append) {

@@ -137,11 +137,13 @@ def test_a_row_of_queries_far_from_the_others():
 @pytest.mark.parametrize("append", [False, True], ids=["plain", "append"])
 @pytest.mark.parametrize("P", [1, 63, 128, 129, 257])
 @pytest.mark.parametrize("shape", [(40, 32, 32, 128), (40, 96, 32, 128), (64, 32, 32, 64),
-                                   (70, 160, 8, 64), (150, 56, 8, 128)],
+                                   (70, 160, 8, 64), (150, 56, 8, 128), (90, 32, 32, 128),
+                                   (100, 96, 32, 128), (160, 32, 32, 64), (300, 8, 8, 128)],
                          ids=lambda s: "b%dH%dK%dD%d" % s)
 def test_many_sequences_behind_a_short_prefix(shape, P, append):
-    """So many that they are split over the SMs, with few tiles of the prefix: groups of 1,
-    3, 7 and 20 heads, tile pairs shared and full, segments of one tile."""
+    """Several sequences a block's SM, and so many that they are split over the SMs with few
+    tiles of the prefix: groups of 1, 3, 7 and 20 heads, tile pairs shared and full, segments
+    of one tile."""
     b, H, Hkv, D = shape
     lens = [(0, 3, 1, 17, 16, 2)[i % 6] for i in range(b)]
     x = inputs(b, H, Hkv, D, P, 17, lens, seed=P + b, append=append)
