@@ -47,8 +47,10 @@ constexpr int BM = 128;      // query rows of a unit (= TMEM lanes)
 constexpr int BN = 128;      // keys of a tile
 constexpr int THREADS = 384;
 constexpr int MAX_CTAS = 148;
-// Ring of K and V tiles: what fits beside two Q tiles.
-__host__ __device__ constexpr int ring(int d) { return d == 128 ? 5 : 10; }
+// Ring of K and V tiles.  Five (what fits beside two Q tiles) streamed a prefix
+// under 16 rows a head at 5.7 TB/s, four at 6.0; three took 2 us more for 32
+// sequences behind 8192 keys.
+__host__ __device__ constexpr int ring(int d) { return d == 128 ? 4 : 8; }
 // The split of 384 x 168 registers: 56 + 224 + 224 a lane.
 constexpr int kRegsControl = 56;
 constexpr int kRegsSoftmax = 224;
