@@ -11,9 +11,16 @@ cos/sin arguments are LLaMA RoPE tables as ``rope_table`` returns them: the
 second half of every row repeats the first (the frequencies concatenated with
 themselves).  The kernels may read either copy; a table whose halves differ
 is not supported (include/llama_attn.h states the same for the C ABI).
+
+``stream``: the work goes to that stream, which the caller has let wait for
+whatever the inputs still wait for, and the inputs stay alive until it is done.
+What the call allocates is made as under ``torch.cuda.stream(stream)``: a block
+of the current stream's pool may still be in use by work queued there.  The
+caller waits for ``stream`` before the current stream reads the outputs.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import math
@@ -190,6 +197,34 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
+def _scratch(like: torch.Tensor, nbytes: int, stream) -> torch.Tensor:
+    """Scratch memory of the stream that will use it: once freed it may only be handed
+    to work that follows there."""
+    if stream is None:
+        return like.new_empty(nbytes, dtype=torch.uint8)
+    with torch.cuda.stream(stream):
+        return like.new_empty(nbytes, dtype=torch.uint8)
+
+
+def _output(like: torch.Tensor, shape, dtype: torch.dtype, stream) -> torch.Tensor:
+    """An output, from the pool of the stream that writes it as scratch is, and noted as
+    used by the caller's stream, which reads it."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(torch.cuda.current_stream(like.device))
+    return t
+
+
+def _positions(pos: torch.Tensor, stream) -> torch.Tensor:
+    """pos as contiguous int64, converted on the stream whose kernel reads it."""
+    if pos.dtype is torch.int64 and pos.is_contiguous():
+        return pos
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        return pos.to(torch.int64).contiguous()
+
+
 def _dtype_code(dt: torch.dtype) -> int:
     if dt == torch.bfloat16:
         return LLAMA_DT_BF16
@@ -202,10 +237,10 @@ def rope_table(pos: torch.Tensor, head_dim: int, theta: float = 10000.0,
                factor: float = 1.0, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """cos, sin [*pos.shape, head_dim] fp32 from int64 positions (llama_rope_table)."""
     lib = load()
-    pos = pos.to(torch.int64).contiguous()
+    pos = _positions(pos, stream)
     n = pos.numel()
-    cos = torch.empty(*pos.shape, head_dim, device=pos.device, dtype=torch.float32)
-    sin = torch.empty_like(cos)
+    cos = _output(pos, (*pos.shape, head_dim), torch.float32, stream)
+    sin = _output(pos, (*pos.shape, head_dim), torch.float32, stream)
     bsz = pos.shape[0] if pos.dim() > 1 else 1
     seq = n // bsz
     _check(lib.llama_rope_table(_ptr(pos), bsz, seq, head_dim, float(theta), float(factor),
@@ -217,10 +252,10 @@ def rope_table_ntk(pos: torch.Tensor, head_dim: int, theta: float = 10000.0, alp
                    stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """cos, sin of the NTK-aware scaled table (llama_rope_table_ntk)."""
     lib = load()
-    pos = pos.to(torch.int64).contiguous()
+    pos = _positions(pos, stream)
     n = pos.numel()
-    cos = torch.empty(*pos.shape, head_dim, device=pos.device, dtype=torch.float32)
-    sin = torch.empty_like(cos)
+    cos = _output(pos, (*pos.shape, head_dim), torch.float32, stream)
+    sin = _output(pos, (*pos.shape, head_dim), torch.float32, stream)
     bsz = pos.shape[0] if pos.dim() > 1 else 1
     seq = n // bsz
     _check(lib.llama_rope_table_ntk(_ptr(pos), bsz, seq, head_dim, float(theta), float(alpha),
@@ -244,24 +279,13 @@ def _on(device: torch.device, where: str, fn, args, stream):
         raise LlamaAttnError(status, where)
 
 
-def _scratch(like: torch.Tensor, nbytes: int, stream) -> torch.Tensor:
-    """Scratch memory of the stream that will use it: once freed it may only be handed
-    to work that follows there."""
-    if stream is None:
-        return like.new_empty(nbytes, dtype=torch.uint8)
-    with torch.cuda.stream(stream):
-        return like.new_empty(nbytes, dtype=torch.uint8)
-
-
 def _table_scaled(where: str, pos: torch.Tensor, head_dim: int, args, stream):
     fn = getattr(_lib or load(), where)
-    if pos.dtype is not torch.int64 or not pos.is_contiguous():
-        with torch.cuda.stream(stream):  # (None: no change) where the kernel reads it
-            pos = pos.to(torch.int64).contiguous()
+    pos = _positions(pos, stream)
     p = _ptr(pos)
     shape, dev = pos.shape, pos.device
-    cos = pos.new_empty((*shape, head_dim), dtype=torch.float32)
-    sin = torch.empty_like(cos)
+    cos = _output(pos, (*shape, head_dim), torch.float32, stream)
+    sin = _output(pos, (*shape, head_dim), torch.float32, stream)
     bsz = shape[0] if len(shape) > 1 else 1
     _on(dev, where, fn, (p, bsz, pos.numel() // max(bsz, 1), head_dim, *args, cos.data_ptr(),
                          sin.data_ptr()), stream)
@@ -336,7 +360,7 @@ def rope_apply(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, si
     qos = kp = ks = kop = kos = None  # (strides of an output made here: dense)
     Hkv = 0
     if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        q_out = _output(q, shape, dt, stream)
         qop = q_out.data_ptr()
     else:
         qop, qos = _rope_view(q_out, w, "out", dt, dev, shape)
@@ -347,7 +371,7 @@ def rope_apply(q: torch.Tensor, k: Optional[torch.Tensor], cos: torch.Tensor, si
         Hkv = k_shape[-2]
         kp, ks = _rope_view(k, w, "k", dt, dev, k_shape)
         if k_out is None:
-            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+            k_out = _output(k, k_shape, dt, stream)
             kop = k_out.data_ptr()
         else:
             kop, kos = _rope_view(k_out, w, "out", dt, dev, k_shape)
@@ -369,9 +393,9 @@ def qkv_rope(x: torch.Tensor, w_qkv: torch.Tensor, n_heads: int, n_kv_heads: int
     _need(w_qkv, w, "w_qkv", x.dtype, x.device, shape=((n_heads + 2 * n_kv_heads) * head_dim, hidden))
     _tables(cos, sin, w, x.device, T, head_dim)
     if out is None:
-        q = torch.empty(T, n_heads, head_dim, device=x.device, dtype=x.dtype)
-        k = torch.empty(T, n_kv_heads, head_dim, device=x.device, dtype=x.dtype)
-        v = torch.empty_like(k)
+        q = _output(x, (T, n_heads, head_dim), x.dtype, stream)
+        k = _output(x, (T, n_kv_heads, head_dim), x.dtype, stream)
+        v = _output(x, (T, n_kv_heads, head_dim), x.dtype, stream)
     else:
         q, k, v = out
         _need(q, w, "q", x.dtype, x.device, numel=T * n_heads * head_dim)
@@ -387,12 +411,13 @@ def out_proj(attn: torch.Tensor, w_o: torch.Tensor, *, out: Optional[torch.Tenso
              stream=None) -> torch.Tensor:
     """llama_attn_out_proj.  attn [T, in], w_o [out, in] -> y [T, out]."""
     lib = load()
-    attn2 = attn.reshape(attn.shape[0], -1)
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        attn2 = attn.reshape(attn.shape[0], -1)  # (a copy, if it takes one, is read there)
     T, d_in = attn2.shape
     d_out = w_o.shape[0]
     _need(w_o, "llama_attn_out_proj", "w_o", attn.dtype, attn.device, shape=(d_out, d_in))
     if out is None:
-        out = torch.empty(T, d_out, device=attn.device, dtype=attn.dtype)
+        out = _output(attn, (T, d_out), attn.dtype, stream)
     _need(out, "llama_attn_out_proj", "out", attn.dtype, attn.device, numel=T * d_out)
     _check(lib.llama_attn_out_proj(_ptr(attn2), _ptr(w_o), T, d_in, d_out, _ptr(out),
                                    _dtype_code(attn.dtype), _stream(stream)), "llama_attn_out_proj")
@@ -425,10 +450,10 @@ def prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty(b, S, H * D, device=q.device, dtype=q.dtype)
+        out = _output(q, (b, S, H * D), q.dtype, stream)
     need = prefill_workspace_bytes(b, H, Hkv, S, D, q.dtype, cos is not None)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+        workspace = _scratch(q, need, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.llama_attn_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(cos), _ptr(sin), b, H, Hkv, S,
                                   D, float(scale), int(bool(causal)), _ptr(out), _ptr(mask),
@@ -453,10 +478,10 @@ def prefill_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty(b, S, H * D, device=q.device, dtype=q.dtype)
+        out = _output(q, (b, S, H * D), q.dtype, stream)
     need = prefill_workspace_bytes(b, H, Hkv, S, D, q.dtype, cos is not None)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+        workspace = _scratch(q, need, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.llama_attn_prefill_window(_ptr(q), _ptr(k), _ptr(v), _ptr(cos), _ptr(sin), b, H,
                                          Hkv, S, D, float(scale), int(window), _ptr(out),
@@ -484,10 +509,10 @@ def prefill_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_lens: 
     if seq_lens.dtype != torch.int32:
         raise ValueError("llama_attn_prefill_varlen: seq_lens must be int32")
     if out is None:
-        out = torch.empty(b, S, H * D, device=q.device, dtype=q.dtype)
+        out = _output(q, (b, S, H * D), q.dtype, stream)
     need = prefill_workspace_bytes(b, H, Hkv, S, D, q.dtype, cos is not None)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+        workspace = _scratch(q, need, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.llama_attn_prefill_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(cos), _ptr(sin),
                                          _ptr(seq_lens), b, H, Hkv, S, D, float(scale),
@@ -518,10 +543,10 @@ def prefill_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens
     if cu_seqlens.dtype != torch.int32:
         raise ValueError("llama_attn_prefill_packed: cu_seqlens must be int32")
     if out is None:
-        out = torch.empty(T, H * D, device=q.device, dtype=q.dtype)
+        out = _output(q, (T, H * D), q.dtype, stream)
     need = prefill_workspace_bytes(1, H, Hkv, T, D, q.dtype, cos is not None)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+        workspace = _scratch(q, need, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.llama_attn_prefill_packed(_ptr(q), _ptr(k), _ptr(v), _ptr(cos), _ptr(sin),
                                          _ptr(cu_seqlens), n, T, int(max_seqlen), H, Hkv, D,
@@ -548,10 +573,9 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty(b, H * D, device=q.device, dtype=q.dtype)
+        out = _output(q, (b, H * D), q.dtype, stream)
     if workspace is None:
-        workspace = torch.empty(decode_workspace_bytes(b, H, L, D), device=q.device,
-                                dtype=torch.uint8)
+        workspace = _scratch(q, decode_workspace_bytes(b, H, L, D), stream)
     ws_bytes = workspace.numel() * workspace.element_size()
     if cache_lens.dtype != torch.int32:
         raise ValueError("llama_attn_decode: cache_lens must be int32")
@@ -581,10 +605,9 @@ def decode_append(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty(b, H * D, device=q.device, dtype=q.dtype)
+        out = _output(q, (b, H * D), q.dtype, stream)
     if workspace is None:
-        workspace = torch.empty(decode_workspace_bytes(b, H, L, D), device=q.device,
-                                dtype=torch.uint8)
+        workspace = _scratch(q, decode_workspace_bytes(b, H, L, D), stream)
     ws_bytes = workspace.numel() * workspace.element_size()
     if cache_lens.dtype != torch.int32:
         raise ValueError("llama_attn_decode_append: cache_lens must be int32")
@@ -683,7 +706,7 @@ def decode_prefix(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tenso
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = q.new_empty((b, H * D))
+        out = _output(q, (b, H * D), dt, stream)
         op = out.data_ptr()
     else:
         op = _ptr(out)
