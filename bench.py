@@ -63,20 +63,19 @@ METRIC = "causal GQA prefill TFLOP/s and KV-decode HBM GB/s, % of B200 roofline"
 
 def _traffic(kernel: str):
     """Per-launch DRAM bytes of `kernel` from the committed ncu record, or None
-    when the CUDA sources changed since that capture."""
-    import glob
+    when a source file that the kernel is made of changed since that capture."""
     import hashlib
     try:
-        rec = json.load(open(os.path.join(ROOT, "profiles", "ncu_traffic.json")))
-    except Exception:
+        rec = json.load(open(os.path.join(ROOT, "profiles", "ncu_traffic.json")))[kernel]
+        h = hashlib.sha256()
+        for name in rec["sources"]:
+            with open(os.path.join(ROOT, "llama_gqa_causal_b200", "csrc", name), "rb") as f:
+                h.update(f.read())
+        if h.hexdigest()[:16] != rec["sources_sha256_16"]:
+            return None
+        return rec["dram_read_bytes"] + rec["dram_write_bytes"]
+    except (OSError, ValueError, KeyError):
         return None
-    h = hashlib.sha256()
-    csrc = os.path.join(ROOT, "llama_gqa_causal_b200", "csrc")
-    for f in sorted(glob.glob(os.path.join(csrc, "*.cu")) + glob.glob(os.path.join(csrc, "*.cuh"))):
-        h.update(open(f, "rb").read())
-    if h.hexdigest()[:16] != rec.get("csrc_sha256_16") or kernel not in rec:
-        return None
-    return rec[kernel]["dram_read_bytes"] + rec[kernel]["dram_write_bytes"]
 
 
 def _peaks():
