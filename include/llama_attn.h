@@ -43,11 +43,12 @@
  *     device memory and never frees what it is given.
  *   - All work is enqueued on `cuda_stream` (a cudaStream_t; NULL = legacy
  *     default stream) and the call returns without synchronising.  Stream
- *     order is kept: the decode kernels and the RoPE table kernel launch as
- *     programmatic dependents of the preceding grid (their blocks may become
- *     resident early) but wait on the device for it to finish before they
- *     read or write any memory.  The
- *     decode combine and the RoPE table kernels allow their own programmatic
+ *     order is kept: the decode kernels, the RoPE table kernels and the
+ *     rotation launch as programmatic dependents of the preceding grid (their
+ *     blocks may become resident early) but wait on the device for it to
+ *     finish before they read or write any memory.  The kernels of
+ *     llama_attn_decode_prefix, the decode combine, the RoPE table kernels and
+ *     the rotation allow their own programmatic
  *     dependents to launch early; a caller kernel launched with the
  *     programmatic-serialization attribute after them must wait
  *     (griddepcontrol.wait / cudaGridDependencySynchronize) before reading
@@ -123,9 +124,12 @@ int llama_rope_table_ntk(const long long* pos, int bsz, int seq, int head_dim, d
  * take the plain frequencies w_i = theta^(-2i/head_dim), i < head_dim/2, and
  * keep the fast ones, which turn many times within the trained length, while
  * the slow ones are divided by `factor`; they differ in how the two are told
- * apart.  Angles are formed in fp64 from pos * w'_i; rows are laid out as
- * llama_rope_table writes them.  head_dim is the number of rotated dimensions
- * (a part of the head, if only that is rotated).
+ * apart.  Angles are formed and reduced in fp64 from pos * w'_i; the entries are
+ * within one step of fp32 (2^-23 of the gain) of the angle's cosine and sine,
+ * where llama_rope_table's are rounded once, so that unscaled frequencies do not
+ * give its table bit for bit.  Rows are laid out as llama_rope_table writes them.
+ * head_dim is the number of rotated dimensions (a part of the head, if only that
+ * is rotated).
  *
  * llama_rope_table_banded: by the number of turns over the trained length,
  *   turns_i = original_len * w_i / (2 pi)

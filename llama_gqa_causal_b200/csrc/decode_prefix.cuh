@@ -30,10 +30,11 @@
 //
 // What bounds it: the prefix part's full tile pairs, like the prefill's tiles, the
 // chain S -> softmax -> P -> P V -> S of either unit, which the other unit's half
-// hides (a pair's 128 keys take 1.85 us an SM, 1.1 PFLOP/s over the chip; the
-// tensor pipe is busy 53 % of the time); shared tile pairs and the own rows,
-// memory.  32 sequences behind 8192 keys with 512 own rows on average (64/8 heads
-// of 128, caches cold): 32 us for 102 MB; 128 behind 32768: 140 us for 139 GFLOP.
+// hides (a pair's 128 keys take 1.96 us an SM, 1.26 PFLOP/s over the chip, by what
+// 128 sequences of 64/8 heads of 128 take more behind 65536 keys than behind
+// 32768); shared tile pairs and the own rows, memory.  32 such sequences behind
+// 8192 keys with 512 own rows on average (caches cold): 33 us for 102 MB; 128
+// behind 32768: 142 us for 139 GFLOP.
 // Few sequences with little behind them are taken whole by a block each
 // (decode_prefix_small_kernel), which saves the second launch and the partials.
 #pragma once
@@ -62,10 +63,10 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // Pairs of 8 exponentiated on the FMA pipe instead of the MUFU: 0, 1 and 2 took
 // 127, 123.5 and 123.5 us for 128 sequences behind 32768 keys.
 constexpr int kPolyPairsOf8 = 1;
-// What one SM takes, in microseconds as a batch of 16 to 128 sequences ran, for
-// an item of a full and of a shared tile pair, a segment's beginning and end (Q,
-// the pipeline's fill, the partial's write), and a step through the own rows.
-// Only their ratios matter.
+// What one SM takes, in microseconds as a mixed batch of 16 to 128 sequences ran
+// (a prefix alone is a little sooner, 1.96 an item), for an item of a full and of a
+// shared tile pair, a segment's beginning and end (Q, the pipeline's fill, the
+// partial's write), and a step through the own rows.  Only their ratios matter.
 __host__ __device__ constexpr float cost_pair(int d) { return d == 128 ? 2.1f : 1.5f; }
 __host__ __device__ constexpr float cost_single(int d) { return d == 128 ? 1.6f : 1.1f; }
 __host__ __device__ constexpr float cost_step(int d) { return d == 128 ? 0.12f : 0.07f; }
@@ -155,7 +156,7 @@ __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
   return d;
 }
 // 2^x for a pair on the FMA and integer pipes, as exp2_poly2 but with a cubic
-// for 2^f (largest relative error 7.5e-5, far below the 2^-9 that rounding the
+// for 2^f (largest relative error 7.5e-5, far below the 2^-8 that rounding the
 // result to bf16 may cost; csrc/fit_exp2_poly.py with degree 3).
 __device__ __forceinline__ void exp2_cubic2(float& y0, float& y1, float x0, float x1) {
   constexpr float kRound = 12582912.0f;  // 1.5 * 2^23

@@ -456,8 +456,12 @@ PrefixLayout prefix_layout(int bsz, int H, int Hkv, int P, int D) {
 // each of them and 6.2 (3.2) a thousand of their rows.  The split has 11 to 13 for
 // two launches and the merge, 1 (0.6) a thousand query rows, 0.03 (0.015) for each
 // CTA that leaves a partial of 256 rows, and its work over the SMs.  Measured
-// both ways from 8 to 1024 sequences and 20 to 4000 rows (208 sizes): the way
-// taken was the faster one or within 20% of it, but for one at 31%.
+// both ways from 8 to 1024 sequences and 20 to 4000 rows (208 sizes), caches half
+// full: the way taken was the faster one or within 20% of it, but for one at 31%.
+// Caches that are nearly empty can get the slower one: 10 own rows in caches of
+// 8192, 4 sequences of 64/8 heads of 128 behind 64 rows 12.5 us split, against 4.3
+// a block each (caches of 4096 and less); 128 of 16/4 heads of 64 behind 2000 rows
+// 27.7 a block each, against 15.7 split.
 int prefix_block_warps(int bsz, int H, int Hkv, int P, int L, int D, long long seqs,
                        const PrefixLayout& w, int n_ctas) {
   using namespace la::px;

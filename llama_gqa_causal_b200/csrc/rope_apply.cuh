@@ -20,7 +20,9 @@ struct ScaledFreqs {
   double inv[ra::kMaxHalf];
 };
 
-// sin and cos of x, |x| < 2^40, to about one step of fp32.  x is reduced in
+// sin and cos of x, |x| < 2^40, to one step of fp32 with the gain's rounding, where
+// the fp64 functions, rounded once, would be off by half a step: 131072 rows of 128
+// take 26.7 us against 68.  x is reduced in
 // fp64 by the nearest multiple k of pi/2, held as a sum of two doubles, to r in
 // [-pi/4, pi/4]; r = rf + rl (rf the nearest float); the Taylor polynomials of
 // sin and cos to r^9 and r^10 (the next terms are below 2^-28 there) are taken
@@ -279,7 +281,10 @@ __global__ void __launch_bounds__(ra::THREADS) rope_apply_vec_kernel(RopeApplyPa
   }
 }
 
-// Any even R, any alignment and strides: a thread per pair or per copied element.
+// Any even R, any alignment and strides: a thread per pair or per copied element,
+// three 64-bit divisions and narrow accesses for each, so far from what its bytes
+// would take: 8192 tokens of 72 heads in bf16, D 96 / R 24 334 us (bytes: 35), D 80
+// / R 20 284 (29), D 80 / R 40 257 (29); in fp32, D 80 / R 20 283 (58).
 template <typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(ra::THREADS) rope_apply_any_kernel(RopeApplyParams p) {
   const int half = p.R / 2;
