@@ -95,3 +95,29 @@ def test_output_dropped_while_the_current_stream_still_reads_it(name):
     torch.cuda.synchronize()
     assert all(torch.equal(k, bits(w)) for k, w in zip(kept, want))
     del later
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_calls_on_a_forked_stream_in_a_capture(name):
+    """A captured fork and join: one output is dropped inside the capture, one is kept."""
+    call, x = CALLS[name], inputs(2)
+    want = tensors(call(x))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        call(x, stream=side)
+        got = tensors(call(x, stream=side))
+        torch.cuda.current_stream().wait_stream(side)
+        copies = [g.clone() for g in got]
+    for _ in range(3):
+        for t in got + copies:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for g, c, w in zip(got, copies, want):
+            assert torch.equal(bits(g), bits(w)) and torch.equal(bits(c), bits(w))
+    again = tensors(call(x, stream=torch.cuda.current_stream()))  # (no other stream at all)
+    torch.cuda.synchronize()
+    assert all(torch.equal(bits(g), bits(w)) for g, w in zip(again, want))
